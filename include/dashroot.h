@@ -454,6 +454,97 @@ dash_status spectral_scale_noalloc(const float* A, float ridge, int64_t N, int B
                                    int n_vec, int power_iters, const float* V0,
                                    float* lambda_out, void* stream);
 
+/*
+ * The operators below stand in front of the preconditioner in a training step: the norm
+ * that feeds a linear layer, the 8-bit checkpoint of its normalised rows, and the linear
+ * layer's weight gradient read from that checkpoint and written in the blocks
+ * shampoo_accumulate takes.  The pages have no counterpart.
+ * Matrices are row-major (rows, cols) with a leading dimension ld >= cols and are
+ * element-aligned, so a view of columns or of every k-th row is fine; vectors are
+ * contiguous.  rows, cols and outs are at most 2^31 - 1.  Every call's results are the
+ * same from run to run: sums run in a fixed order.
+ *
+ * act_compress / act_restore -- a matrix to its 8-bit checkpoint and back.
+ * A row is cut into groups of 32 columns, G = ceil(cols / 32), the last one padded with
+ * zeros.  A group has one scale 2^e and 32 codes; its values are code * 2^e, with
+ *   DASH_Q8_INT8  codes -127 .. 127,   e = floor(log2 amax) - 6, plus 1 where amax 2^-e
+ *                 would round to 128; e in [-124, 121];
+ *   DASH_Q8_E4M3  codes of 4 exponent and 3 mantissa bits up to 448, e = floor(log2 amax)
+ *                 - 8, plus 1 where amax 2^-e > 464; e in [-124, 119];
+ * amax the group's largest magnitude.  Every value is rounded once, to the nearest code,
+ * ties to even.  Stored are q (rows, 32 G) bytes, contiguous and 16-byte aligned, and
+ * scale (rows, G) bytes, e + 127.  Every value is a finite bf16 number exactly.  A group
+ * holding an infinity or a NaN gets the scale byte 255 and reads back as NaN, all of it.
+ *   act_restore writes the values in dtype dt (rounded once where dt cannot hold them).
+ */
+typedef enum { DASH_Q8_INT8 = 0, DASH_Q8_E4M3 = 1 } dash_q8;
+
+dash_status act_compress(const void* x, int dt, int64_t rows, int64_t cols, int64_t ld, int fmt,
+                         uint8_t* q, uint8_t* scale, void* stream);
+dash_status act_restore(const uint8_t* q, const uint8_t* scale, int fmt, int64_t rows,
+                        int64_t cols, void* x, int dt, int64_t ld, void* stream);
+
+/*
+ * layer_norm_forward -- per row of x (rows, cols), dtype dt:
+ *   r = x + residual (rounded to dt; r = x without a residual),
+ *   mean = sum(r) / cols, rstd = (sum((r - mean)^2) / cols + eps)^(-1/2),
+ *   n = (r - mean) rstd,  y = n gamma + beta.
+ * center = 0 takes mean = 0 (the root-mean-square norm).  Sums, mean, rstd and n are fp32.
+ *   residual, gamma (1), beta (0), r, mean, rstd, q / scale may be NULL; gamma and beta
+ *   (cols,) have dtype wdt, mean and rstd (rows,) are fp32, y and r have dtype dt.  r may
+ *   be x or residual (in place).  q / scale receive n's checkpoint in format fmt.
+ *   cols <= DASH_NORM_MAX_COLS, else DASH_ERR_UNSUPPORTED; eps finite and >= 0.  rows or
+ *   cols = 0 is a no-op.
+ */
+#define DASH_NORM_MAX_COLS 16384
+dash_status layer_norm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldres,
+                               int dt, int64_t rows, int64_t cols, const void* gamma,
+                               const void* beta, int wdt, float eps, int center, void* r,
+                               int64_t ldr, void* y, int64_t ldy, float* mean, float* rstd,
+                               int fmt, uint8_t* q, uint8_t* scale, void* stream);
+
+/*
+ * layer_norm_backward -- the gradients of layer_norm_forward:
+ *   g = dy gamma,  c1 = sum(g) / cols (0 with center = 0),  c2 = sum(g n) / cols,
+ *   dx = rstd (g - c1 - n c2) + dres,
+ *   dgamma = sum over rows of dy n,  dbeta = sum over rows of dy.
+ * n comes either from its checkpoint (q, scale, fmt) or from the norm's input x (the r of
+ * the forward pass) with mean (needed with center != 0) and rstd: exactly one of x and q
+ * is given.  dres, the gradient that bypasses the norm, gamma, dgamma and dbeta may be
+ * NULL.  dx has dtype dt and may be dy or dres (in place); dgamma and dbeta (cols,) are
+ * fp32.  rows = 0 sets dgamma and dbeta to 0.
+ * Workspace (for dgamma / dbeta): dash_layer_norm_workspace_size(rows, cols); a smaller
+ * one is DASH_ERR_WORKSPACE_TOO_SMALL.
+ */
+dash_status layer_norm_backward(const void* dy, int64_t lddy, int dt, int64_t rows, int64_t cols,
+                                const void* x, int64_t ldx, const float* mean, const uint8_t* q,
+                                const uint8_t* scale, int fmt, const float* rstd,
+                                const void* gamma, int wdt, int center, const void* dres,
+                                int64_t lddres, void* dx, int64_t lddx, float* dgamma,
+                                float* dbeta, void* ws, size_t ws_bytes, void* stream);
+dash_status dash_layer_norm_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/*
+ * weight_grad -- the weight gradient of z = W (n gamma + beta) + b, W (outs, cols), over
+ * `rows` tokens, with the normalised input n read from its checkpoint:
+ *   dW[o][i] = gamma[i] sum_t dz[t][o] n[t][i] + beta[i] db[o],  db[o] = sum_t dz[t][o].
+ * (Without gamma and beta: the weight gradient of a layer whose input itself was kept by
+ * act_compress.)  dz (rows, outs) has dtype dt; dW has dtype odt and is a matrix (outs,
+ * cols) with leading dimension ldw for B = 0, else the zero-padded row-block-major
+ * (ceil(outs / B) * ceil(cols / B), B, B) stack that pack_blocks would make of it
+ * (B as for every stack; ldw ignored).  gamma, beta and db (outs,) fp32 may be NULL.
+ * rows = 0 gives zeros; outs or cols = 0 is a no-op.  The products are exact (n is bf16,
+ * and dz enters as one, two or three bf16 parts that add up to it), sums are fp32.
+ * Workspace: dash_weight_grad_workspace_size; a smaller one is
+ * DASH_ERR_WORKSPACE_TOO_SMALL.
+ */
+dash_status weight_grad(const void* dz, int dt, int64_t lddz, int64_t rows, int64_t outs,
+                        const uint8_t* q, const uint8_t* scale, int fmt, int64_t cols,
+                        const void* gamma, const void* beta, int wdt, void* dW, int odt,
+                        int64_t ldw, int B, float* db, void* ws, size_t ws_bytes, void* stream);
+dash_status dash_weight_grad_workspace_size(int64_t rows, int64_t outs, int64_t cols, int dt,
+                                            int B, size_t* bytes);
+
 /* Workspace bytes for op on N blocks of order B (param: iters for CN/NDB,
  * degree for Chebyshev, n_vec for spectral_scale; gdt for accumulate/apply is
  * taken from prec: pass DASH_FP32_3XTF32 for fp32 gradients). */
@@ -485,7 +576,9 @@ typedef enum {
   DASH_TRACE_ELEMENTWISE = 4,
   DASH_TRACE_POWER = 5,
   DASH_TRACE_REDUCE = 6,
-  DASH_TRACE_PACK = 7
+  DASH_TRACE_PACK = 7,
+  DASH_TRACE_NORM = 8,
+  DASH_TRACE_CHECKPOINT = 9
 } dash_trace_kind;
 
 dash_status dash_trace_start(int capacity);

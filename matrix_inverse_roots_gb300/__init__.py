@@ -10,6 +10,7 @@ computation runs in the library's CUDA kernels.  There is no fallback: if
 ``libdashroot.so`` is missing the first call raises.
 """
 
+import collections
 import ctypes
 import os
 
@@ -33,6 +34,13 @@ ROOT_TF32 = 0x100
 DT_F32 = 0
 DT_BF16 = 1
 DT_F16 = 2
+
+# dash_q8: formats of an 8-bit activation checkpoint
+Q8_INT8 = 0
+Q8_E4M3 = 1
+Q8_FORMATS = {"int8": Q8_INT8, "e4m3": Q8_E4M3}
+Q8_GROUP = 32  # columns that share a scale
+NORM_MAX_COLS = 16384
 
 # dash_scale_mode
 SCALE_POWER = 0
@@ -82,7 +90,9 @@ SYMBOLS = (
     "dash_trace_count", "dash_trace_read", "dash_trace_stop", "spectral_scale_noalloc",
     "dash_selftest_wait_timeout", "precondition_update", "pack_blocks", "unpack_blocks",
     "dash_cheb_coeffs", "dash_select_tiers", "spectral_lambda_min", "inv_root_auto",
-    "dash_auto_workspace_size", "dash_gemm_ex",
+    "dash_auto_workspace_size", "dash_gemm_ex", "act_compress", "act_restore",
+    "layer_norm_forward", "layer_norm_backward", "dash_layer_norm_workspace_size",
+    "weight_grad", "dash_weight_grad_workspace_size",
 )
 
 _lib = None
@@ -115,6 +125,16 @@ def load_library(path=None):
     lib.precondition_update.argtypes = [vp, i32, vp, i64, i32, i32, f32, vp, vp, vp, sz, vp]
     lib.pack_blocks.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp]
     lib.unpack_blocks.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp]
+    lib.act_compress.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
+    lib.act_restore.argtypes = [vp, vp, i32, i64, i64, vp, i32, i64, vp]
+    lib.layer_norm_forward.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, vp, i32, f32, i32, vp,
+                                       i64, vp, i64, vp, vp, i32, vp, vp, vp]
+    lib.layer_norm_backward.argtypes = [vp, i64, i32, i64, i64, vp, i64, vp, vp, vp, i32, vp, vp,
+                                        i32, i32, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+    lib.dash_layer_norm_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+    lib.weight_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, vp, vp, i32, vp, i32,
+                                i64, i32, vp, vp, sz, vp]
+    lib.dash_weight_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(sz)]
     lib.dash_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp]
     lib.dash_workspace_size.argtypes = [i32, i64, i32, i32, i32, ctypes.POINTER(sz)]
     lib.dash_op_matmuls.argtypes = [i32, i32]
@@ -150,7 +170,10 @@ def load_library(path=None):
     lib.dash_trace_stop.argtypes = []
     for name in ("shampoo_accumulate", "spectral_scale", "inv_root_cn", "inv_root_ndb",
                  "inv_root_cheb", "precondition_apply", "precondition_update", "pack_blocks",
-                 "unpack_blocks", "dash_gemm", "dash_workspace_size",
+                 "unpack_blocks", "dash_gemm", "dash_workspace_size", "act_compress",
+                 "act_restore", "layer_norm_forward", "layer_norm_backward",
+                 "dash_layer_norm_workspace_size", "weight_grad",
+                 "dash_weight_grad_workspace_size",
                  "dash_device_status", "dash_trace_start", "dash_trace_read", "dash_trace_stop"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
@@ -176,6 +199,15 @@ def _ptr(t):
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _addr(t):
+    """Device address of an optional tensor argument."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream():
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _stack(t, name, dtype=torch.float32):
@@ -252,7 +284,7 @@ def workspace(op, n, b, prec=FP32_3XTF32, param=0, device=None, max_bytes=None):
 
 # dash_trace_kind
 TRACE_KINDS = ("gemm_f16", "gemm_bf16", "gemm_tf32", "gemm_3xtf32", "elementwise", "power",
-               "reduce", "pack")
+               "reduce", "pack", "norm", "checkpoint")
 
 
 def trace_start(capacity=4096):
@@ -582,6 +614,239 @@ def unpack_blocks(blocks, rows, cols, out=None):
     _check(lib.unpack_blocks(_ptr(blocks), _gdt(blocks), rows, cols, out.stride(0), B, _ptr(out),
                              _stream()), "unpack_blocks")
     return out
+
+
+# ---------------------------------------------------------------- training operators
+
+
+def _fmt(fmt):
+    if fmt not in Q8_FORMATS:
+        raise ValueError("checkpoint format must be one of %s, got %r"
+                         % (sorted(Q8_FORMATS), fmt))
+    return Q8_FORMATS[fmt]
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """A (rows, cols) matrix with unit column stride on the current device: (ld, dtype
+    code).  Rows may lie further apart than cols, not closer."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise TypeError("%s must be a 2-D CUDA tensor" % name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s but the current CUDA device is cuda:%d" % (
+            name, t.device, torch.cuda.current_device()))
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, (rows, cols)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if ld < cols:
+        if rows > 1:
+            raise ValueError("the rows of %s overlap" % name)
+        ld = cols
+    return ld, _DTYPES.get(t.dtype, -1)
+
+
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+
+
+def _vec(t, n, name, dtype=None):
+    _stack(t, name, dtype or t.dtype)
+    return _shape(t, (n,), name)
+
+
+def _codes(q, scale, rows, cols):
+    ng = -(-cols // Q8_GROUP)
+    _shape(_stack(q, "q", torch.uint8), (rows, ng * Q8_GROUP), "q")
+    _shape(_stack(scale, "scale", torch.uint8), (rows, ng), "scale")
+
+
+def _empty_codes(rows, cols, device):
+    ng = -(-cols // Q8_GROUP)
+    return (torch.empty((rows, ng * Q8_GROUP), dtype=torch.uint8, device=device),
+            torch.empty((rows, ng), dtype=torch.uint8, device=device))
+
+
+def act_compress(x, fmt="int8", q=None, scale=None):
+    """The 8-bit checkpoint of a matrix x (rows, cols): (q, scale), uint8 tensors of
+    (rows, 32 G) codes and (rows, G) scale bytes, G = ceil(cols / 32).  fmt: "int8" or
+    "e4m3".  x may be a row-strided view."""
+    lib = load_library()
+    f = _fmt(fmt)
+    ld, dt = _rows(x, "x")
+    rows, cols = x.shape
+    if q is None and scale is None:
+        q, scale = _empty_codes(rows, cols, x.device)
+    else:
+        _codes(q, scale, rows, cols)
+    _check(lib.act_compress(x.data_ptr(), dt, rows, cols, ld, f, q.data_ptr(), scale.data_ptr(),
+                            _raw_stream()), "act_compress")
+    return q, scale
+
+
+def act_restore(q, scale, cols, fmt="int8", dtype=torch.bfloat16, out=None):
+    """The values of a checkpoint, (rows, cols) in `dtype`; `out` may be a row-strided view
+    (its dtype is then the one written)."""
+    lib = load_library()
+    f = _fmt(fmt)
+    if not isinstance(scale, torch.Tensor) or scale.dim() != 2:
+        raise ValueError("scale must be a (rows, G) tensor")
+    rows = scale.shape[0]
+    _codes(q, scale, rows, cols)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=q.device)
+    ld, dt = _rows(out, "out", None, (rows, cols))
+    _check(lib.act_restore(q.data_ptr(), scale.data_ptr(), f, rows, cols, out.data_ptr(), dt, ld,
+                           _raw_stream()), "act_restore")
+    return out
+
+
+# What layer_norm_forward returns; what was not asked for is None.
+NormForward = collections.namedtuple("NormForward", "y mean rstd r q scale")
+
+
+def layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, center=True, residual=None, ckpt=None,
+                       stats=True, y=None, r=None):
+    """y = n gamma + beta with n = (r - mean) rstd over the columns, r = x + residual;
+    center=False leaves the mean out (the root-mean-square norm).
+
+    Returns NormForward(y, mean, rstd, r, q, scale): mean (None without center) and rstd if
+    stats, r if a residual is given, q and scale (n's checkpoint) if ckpt is "int8" or
+    "e4m3".  gamma and beta share a dtype.  r may be x or residual (in place)."""
+    lib = load_library()
+    ldx, dt = _rows(x, "x")
+    rows, cols = x.shape
+    dev, shape = x.device, (rows, cols)
+    wdt = DT_F32
+    if gamma is not None:
+        wdt = _gdt(_vec(gamma, cols, "gamma"))
+    if beta is not None:
+        wdt = _gdt(_vec(beta, cols, "beta", None if gamma is None else gamma.dtype))
+    ldres = ldr = 0
+    if residual is not None:
+        ldres, _ = _rows(residual, "residual", x.dtype, shape)
+        if r is None:
+            r = torch.empty(shape, dtype=x.dtype, device=dev)
+    if r is not None:
+        ldr, _ = _rows(r, "r", x.dtype, shape)
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=dev)
+    ldy, _ = _rows(y, "y", x.dtype, shape)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats and center else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
+    q = scale = None
+    f = Q8_INT8
+    if ckpt is not None:
+        f = _fmt(ckpt)
+        q, scale = _empty_codes(rows, cols, dev)
+    _check(lib.layer_norm_forward(x.data_ptr(), ldx, _addr(residual), ldres, dt, rows, cols,
+                                  _addr(gamma), _addr(beta), wdt, eps, 1 if center else 0,
+                                  _addr(r), ldr, y.data_ptr(), ldy, _addr(mean), _addr(rstd), f,
+                                  _addr(q), _addr(scale), _raw_stream()), "layer_norm_forward")
+    return NormForward(y, mean, rstd, r, q, scale)
+
+
+def layer_norm_workspace_size(rows, cols):
+    out = ctypes.c_size_t(0)
+    _check(load_library().dash_layer_norm_workspace_size(int(rows), int(cols), ctypes.byref(out)),
+           "dash_layer_norm_workspace_size")
+    return out.value
+
+
+def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=None, fmt="int8",
+                        center=True, dres=None, beta=True, dx=None, ws=None):
+    """The gradients (dx, dgamma, dbeta) of layer_norm_forward.
+
+    The normalised rows are read from their checkpoint (q, scale, fmt) or formed from the
+    norm's input x (the forward's r), mean and rstd.  dres, the gradient that bypasses the
+    norm, is added to dx.  dgamma is None without gamma, dbeta with beta=False; both are
+    fp32.  dx may be dy or dres (in place)."""
+    lib = load_library()
+    lddy, dt = _rows(dy, "dy")
+    rows, cols = dy.shape
+    dev, shape = dy.device, (rows, cols)
+    _vec(rstd, rows, "rstd", torch.float32)
+    f = _fmt(fmt)
+    ldx = lddres = 0
+    if (x is None) == (q is None):
+        raise ValueError("give the norm's input x or its checkpoint (q, scale), not both")
+    if q is not None:
+        _codes(q, scale, rows, cols)
+        mean = None
+    else:
+        ldx, _ = _rows(x, "x", dy.dtype, shape)
+        if center:
+            if mean is None:
+                raise ValueError("mean is needed with x and center")
+            _vec(mean, rows, "mean", torch.float32)
+    wdt = DT_F32
+    dgamma = dbeta = None
+    if gamma is not None:
+        wdt = _gdt(_vec(gamma, cols, "gamma"))
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
+    if beta:
+        dbeta = torch.empty(cols, dtype=torch.float32, device=dev)
+    if dres is not None:
+        lddres, _ = _rows(dres, "dres", dy.dtype, shape)
+    if dx is None:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
+    lddx, _ = _rows(dx, "dx", dy.dtype, shape)
+    if ws is None and (gamma is not None or beta):
+        ws = torch.empty(max(layer_norm_workspace_size(rows, cols), 256), dtype=torch.uint8,
+                         device=dev)
+    _check(lib.layer_norm_backward(dy.data_ptr(), lddy, dt, rows, cols, _addr(x), ldx, _addr(mean),
+                                   _addr(q), _addr(scale), f, rstd.data_ptr(), _addr(gamma), wdt,
+                                   1 if center else 0, _addr(dres), lddres, dx.data_ptr(), lddx,
+                                   _addr(dgamma), _addr(dbeta), _addr(ws), _nbytes(ws),
+                                   _raw_stream()), "layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def weight_grad_workspace_size(rows, outs, cols, dtype=torch.bfloat16, B=None):
+    out = ctypes.c_size_t(0)
+    _check(load_library().dash_weight_grad_workspace_size(
+        int(rows), int(outs), int(cols), _DTYPES.get(dtype, -1), int(B or 0), ctypes.byref(out)),
+        "dash_weight_grad_workspace_size")
+    return out.value
+
+
+def weight_grad(dz, q, scale, cols, fmt="int8", gamma=None, beta=None, B=None, dtype=None,
+                bias=False, out=None, ws=None):
+    """(dW, db) of a linear layer z = W (n gamma + beta) + b from dz (rows, outs) and the
+    checkpoint of n: dW = dz^T (n gamma + beta), db = the column sums of dz (fp32; None
+    unless bias).  dW has `dtype` (dz's by default) and is (outs, cols), or with B the
+    zero-padded row-block-major (N, B, B) blocks of it, as pack_blocks cuts them."""
+    lib = load_library()
+    f = _fmt(fmt)
+    lddz, dt = _rows(dz, "dz")
+    rows, outs = dz.shape
+    dev = dz.device
+    _codes(q, scale, rows, cols)
+    wdt = DT_F32
+    if gamma is not None:
+        wdt = _gdt(_vec(gamma, cols, "gamma"))
+    if beta is not None:
+        wdt = _gdt(_vec(beta, cols, "beta", None if gamma is None else gamma.dtype))
+    b = int(B or 0)
+    if out is None:
+        dtype = dtype or dz.dtype
+        shape = (outs, cols) if not b else (-(-outs // b) * -(-cols // b), b, b)
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    if b:
+        _shape(_stack(out, "out", out.dtype), (-(-outs // b) * -(-cols // b), b, b), "out")
+        ldw = 0
+    else:
+        ldw, _ = _rows(out, "out", None, (outs, cols))
+    db = torch.empty(outs, dtype=torch.float32, device=dev) if bias else None
+    if ws is None:
+        ws = torch.empty(max(weight_grad_workspace_size(rows, outs, cols, dz.dtype, b), 256),
+                         dtype=torch.uint8, device=dev)
+    _check(lib.weight_grad(dz.data_ptr(), dt, lddz, rows, outs, q.data_ptr(), scale.data_ptr(), f,
+                           cols, _addr(gamma), _addr(beta), wdt, out.data_ptr(), _gdt(out), ldw, b,
+                           _addr(db), ws.data_ptr(), _nbytes(ws), _raw_stream()), "weight_grad")
+    return out, db
 
 
 def gemm(A, B, prec=TF32, trans_a=False, trans_b=False, A_lo=None, B_lo=None, C=None):

@@ -1,0 +1,155 @@
+// C-ABI entry points of the training operators: argument checks and workspace carving.
+#include <cmath>
+
+#include "dash_internal.h"
+#include "dashroot.h"
+#include "train_internal.h"
+
+using namespace dash;
+
+namespace {
+
+constexpr int64_t MAX_ROWS = 0x7fffffff;
+
+bool valid_dt(int dt) { return dt == DASH_DT_F32 || dt == DASH_DT_BF16 || dt == DASH_DT_F16; }
+bool valid_fmt(int f) { return f == DASH_Q8_INT8 || f == DASH_Q8_E4M3; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// A matrix argument: element-aligned, rows at least `cols` elements apart.
+bool valid_matrix(const void* p, int dt, int64_t cols, int64_t ld) {
+  return p != nullptr && aligned(p, dt_bytes(dt)) && ld >= cols;
+}
+bool optional_matrix(const void* p, int dt, int64_t cols, int64_t ld) {
+  return p == nullptr || valid_matrix(p, dt, cols, ld);
+}
+bool optional_vector(const void* p, int dt) {
+  return p == nullptr || aligned(p, static_cast<uintptr_t>(dt_bytes(dt)));
+}
+bool valid_sizes(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows <= MAX_ROWS && cols <= MAX_ROWS;
+}
+bool valid_codes(const uint8_t* q, const uint8_t* scale) {
+  return q != nullptr && scale != nullptr && aligned(q, 16);
+}
+
+}  // namespace
+
+extern "C" {
+
+dash_status act_compress(const void* x, int dt, int64_t rows, int64_t cols, int64_t ld, int fmt,
+                         uint8_t* q, uint8_t* scale, void* stream) {
+  if (!valid_dt(dt) || !valid_fmt(fmt) || !valid_sizes(rows, cols) || ld < cols)
+    return DASH_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return DASH_OK;
+  if (!valid_matrix(x, dt, cols, ld) || !valid_codes(q, scale)) return DASH_ERR_INVALID_ARG;
+  const CompressArgs a = {x, dt, rows, cols, ld, fmt, q, scale};
+  return launch_act_compress(a, static_cast<cudaStream_t>(stream));
+}
+
+dash_status act_restore(const uint8_t* q, const uint8_t* scale, int fmt, int64_t rows,
+                        int64_t cols, void* x, int dt, int64_t ld, void* stream) {
+  if (!valid_dt(dt) || !valid_fmt(fmt) || !valid_sizes(rows, cols) || ld < cols)
+    return DASH_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return DASH_OK;
+  if (!valid_matrix(x, dt, cols, ld) || !valid_codes(q, scale)) return DASH_ERR_INVALID_ARG;
+  const RestoreArgs a = {q, scale, fmt, rows, cols, x, dt, ld};
+  return launch_act_restore(a, static_cast<cudaStream_t>(stream));
+}
+
+dash_status layer_norm_forward(const void* x, int64_t ldx, const void* residual, int64_t ldres,
+                               int dt, int64_t rows, int64_t cols, const void* gamma,
+                               const void* beta, int wdt, float eps, int center, void* r,
+                               int64_t ldr, void* y, int64_t ldy, float* mean, float* rstd,
+                               int fmt, uint8_t* q, uint8_t* scale, void* stream) {
+  if (!valid_dt(dt) || !valid_dt(wdt) || !valid_fmt(fmt) || !valid_sizes(rows, cols) ||
+      !std::isfinite(eps) || eps < 0.0f)
+    return DASH_ERR_INVALID_ARG;
+  if (cols > DASH_NORM_MAX_COLS) return DASH_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return DASH_OK;
+  if (!valid_matrix(x, dt, cols, ldx) || !optional_matrix(residual, dt, cols, ldres) ||
+      !optional_matrix(r, dt, cols, ldr) || !valid_matrix(y, dt, cols, ldy) ||
+      !optional_vector(gamma, wdt) || !optional_vector(beta, wdt) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || (q != nullptr) != (scale != nullptr) || !aligned(q, 16))
+    return DASH_ERR_INVALID_ARG;
+  const NormFwdArgs a = {x,   ldx,    residual, ldres, dt, rows, static_cast<int>(cols),
+                         gamma, beta, wdt,      eps,   center != 0, r, ldr, y, ldy,
+                         mean, rstd,  fmt,      q,     scale};
+  return launch_norm_forward(a, static_cast<cudaStream_t>(stream));
+}
+
+dash_status dash_layer_norm_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+  if (bytes == nullptr || !valid_sizes(rows, cols)) return DASH_ERR_INVALID_ARG;
+  if (cols > DASH_NORM_MAX_COLS) return DASH_ERR_UNSUPPORTED;
+  *bytes = norm_backward_ws(rows, cols);
+  return DASH_OK;
+}
+
+dash_status layer_norm_backward(const void* dy, int64_t lddy, int dt, int64_t rows, int64_t cols,
+                                const void* x, int64_t ldx, const float* mean, const uint8_t* q,
+                                const uint8_t* scale, int fmt, const float* rstd,
+                                const void* gamma, int wdt, int center, const void* dres,
+                                int64_t lddres, void* dx, int64_t lddx, float* dgamma,
+                                float* dbeta, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dt(dt) || !valid_dt(wdt) || !valid_fmt(fmt) || !valid_sizes(rows, cols))
+    return DASH_ERR_INVALID_ARG;
+  if (cols > DASH_NORM_MAX_COLS) return DASH_ERR_UNSUPPORTED;
+  if (cols == 0) return DASH_OK;
+  if (!optional_vector(gamma, wdt) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
+    return DASH_ERR_INVALID_ARG;
+  if (rows > 0) {
+    // The normalised rows come from the input or from its checkpoint, not both.
+    if (!valid_matrix(dy, dt, cols, lddy) || (x != nullptr) == (q != nullptr) ||
+        !optional_matrix(x, dt, cols, ldx) || !optional_matrix(dres, dt, cols, lddres) ||
+        !valid_matrix(dx, dt, cols, lddx) || rstd == nullptr || !aligned(rstd, 4))
+      return DASH_ERR_INVALID_ARG;
+    if (q != nullptr && !valid_codes(q, scale)) return DASH_ERR_INVALID_ARG;
+    if (x != nullptr && center && (mean == nullptr || !aligned(mean, 4)))
+      return DASH_ERR_INVALID_ARG;
+  }
+  if (dgamma != nullptr || dbeta != nullptr) {
+    if (ws_bytes < norm_backward_ws(rows, cols)) return DASH_ERR_WORKSPACE_TOO_SMALL;
+    if (ws == nullptr || !aligned(ws, 256)) return DASH_ERR_INVALID_ARG;
+  }
+  const NormBwdArgs a = {dy, lddy, dt,  rows, static_cast<int>(cols), x, ldx, mean,
+                         q,  scale, fmt, rstd, gamma, wdt, center != 0, dres, lddres, dx, lddx,
+                         dgamma, dbeta};
+  return launch_norm_backward(a, ws, static_cast<cudaStream_t>(stream));
+}
+
+dash_status dash_weight_grad_workspace_size(int64_t rows, int64_t outs, int64_t cols, int dt,
+                                            int B, size_t* bytes) {
+  if (bytes == nullptr || !valid_sizes(rows, cols) || !valid_sizes(rows, outs) || !valid_dt(dt) ||
+      (B != 0 && (B < 128 || B > 2048 || B % 128 != 0)))
+    return DASH_ERR_INVALID_ARG;
+  WeightGradArgs a = {};
+  a.dt = dt;
+  a.rows = rows;
+  a.outs = outs;
+  a.cols = cols;
+  a.block = B;
+  *bytes = weight_grad_ws(a);
+  return DASH_OK;
+}
+
+dash_status weight_grad(const void* dz, int dt, int64_t lddz, int64_t rows, int64_t outs,
+                        const uint8_t* q, const uint8_t* scale, int fmt, int64_t cols,
+                        const void* gamma, const void* beta, int wdt, void* dW, int odt,
+                        int64_t ldw, int B, float* db, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dt(dt) || !valid_dt(wdt) || !valid_dt(odt) || !valid_fmt(fmt) ||
+      !valid_sizes(rows, cols) || !valid_sizes(rows, outs) ||
+      (B != 0 && (B < 128 || B > 2048 || B % 128 != 0)))
+    return DASH_ERR_INVALID_ARG;
+  if (outs == 0 || cols == 0) return DASH_OK;
+  if (dW == nullptr || !aligned(dW, dt_bytes(odt)) || (B == 0 && ldw < cols) ||
+      !optional_vector(gamma, wdt) || !optional_vector(beta, wdt) || !aligned(db, 4))
+    return DASH_ERR_INVALID_ARG;
+  if (rows > 0 && (!valid_matrix(dz, dt, outs, lddz) || !valid_codes(q, scale)))
+    return DASH_ERR_INVALID_ARG;
+  const WeightGradArgs a = {dz, dt, lddz, rows, outs, q, scale, fmt, cols, gamma, beta, wdt,
+                            dW, odt, ldw, B, db};
+  if (ws_bytes < weight_grad_ws(a)) return DASH_ERR_WORKSPACE_TOO_SMALL;
+  if (ws == nullptr || !aligned(ws, 256)) return DASH_ERR_INVALID_ARG;
+  return launch_weight_grad(a, ws, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

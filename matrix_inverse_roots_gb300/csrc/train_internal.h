@@ -1,0 +1,112 @@
+// Host-side interfaces of the training operators (train_api.cu) to their kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dashroot.h"
+
+namespace dash {
+
+struct CompressArgs {
+  const void* x;
+  int dt;
+  long long rows, cols, ld;
+  int fmt;
+  uint8_t* q;
+  uint8_t* scale;
+};
+dash_status launch_act_compress(const CompressArgs& a, cudaStream_t st);
+
+struct RestoreArgs {
+  const uint8_t* q;
+  const uint8_t* scale;
+  int fmt;
+  long long rows, cols;
+  void* x;
+  int dt;
+  long long ld;
+};
+dash_status launch_act_restore(const RestoreArgs& a, cudaStream_t st);
+
+struct NormFwdArgs {
+  const void* x;
+  long long ldx;
+  const void* residual;  // null: none
+  long long ldres;
+  int dt;
+  long long rows;
+  int cols;
+  const void* gamma;  // null: 1
+  const void* beta;   // null: 0
+  int wdt;
+  float eps;
+  int center;
+  void* r;  // null: not stored
+  long long ldr;
+  void* y;
+  long long ldy;
+  float* mean;  // null: not stored
+  float* rstd;  // null: not stored
+  int fmt;
+  uint8_t* q;  // null: no checkpoint
+  uint8_t* scale;
+};
+dash_status launch_norm_forward(const NormFwdArgs& a, cudaStream_t st);
+
+struct NormBwdArgs {
+  const void* dy;
+  long long lddy;
+  int dt;
+  long long rows;
+  int cols;
+  const void* x;  // the norm's input, or null: the checkpoint q / scale
+  long long ldx;
+  const float* mean;
+  const uint8_t* q;
+  const uint8_t* scale;
+  int fmt;
+  const float* rstd;
+  const void* gamma;
+  int wdt;
+  int center;
+  const void* dres;  // null: none
+  long long lddres;
+  void* dx;
+  long long lddx;
+  float* dgamma;  // null: not wanted
+  float* dbeta;   // null: not wanted
+};
+size_t norm_backward_ws(long long rows, long long cols);
+dash_status launch_norm_backward(const NormBwdArgs& a, void* ws, cudaStream_t st);
+
+struct WeightGradArgs {
+  const void* dz;
+  int dt;
+  long long lddz;
+  long long rows, outs;
+  const uint8_t* q;
+  const uint8_t* scale;
+  int fmt;
+  long long cols;
+  const void* gamma;  // null: 1
+  const void* beta;   // null: 0
+  int wdt;
+  void* dw;
+  int odt;
+  long long ldw;
+  int block;  // 0: a matrix; else the order of the blocks
+  float* db;  // null: not wanted
+};
+size_t weight_grad_ws(const WeightGradArgs& a);
+dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t st);
+
+// Column sums, in fp32 and in a fixed order, of a (rows, cols) matrix of dtype dt:
+// out[c] = sum_r m[r][c].  part holds col_sum_parts(rows, cols) rows of cols floats.
+int col_sum_parts(long long rows, long long cols);
+dash_status launch_col_sum(const void* m, int dt, long long rows, long long cols, long long ld,
+                           float* part, float* out, cudaStream_t st);
+
+inline int dt_bytes(int dt) { return dt == DASH_DT_F32 ? 4 : 2; }
+
+}  // namespace dash

@@ -42,8 +42,10 @@ from .roots64 import (
 )
 from .select64 import (DEFAULT_TIERS, auto_inv_root, condition_estimate, lambda_min_estimate,
                        select_tiers)
+from . import train64
 
 __all__ = [
+    "train64",
     "accumulate",
     "apply_preconditioner",
     "frobenius_norm",
