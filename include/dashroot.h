@@ -535,7 +535,10 @@ dash_status dash_layer_norm_workspace_size(int64_t rows, int64_t cols, size_t* b
  * (B as for every stack; ldw ignored).  gamma, beta and db (outs,) fp32 may be NULL.
  * rows = 0 gives zeros; outs or cols = 0 is a no-op.  The products are exact (n is bf16,
  * and dz enters as one, two or three bf16 parts that add up to it), sums are fp32.
- * Workspace: dash_weight_grad_workspace_size; a smaller one is
+ * A stack dW is 16-byte aligned.
+ * Workspace: dash_weight_grad_workspace_size, with the lddz of a dz whose address is a
+ * multiple of 16 bytes, or 0 for any other dz (its parts are then laid out in the
+ * workspace, as those of fp16 and fp32 always are); a smaller one is
  * DASH_ERR_WORKSPACE_TOO_SMALL.
  */
 dash_status weight_grad(const void* dz, int dt, int64_t lddz, int64_t rows, int64_t outs,
@@ -543,7 +546,7 @@ dash_status weight_grad(const void* dz, int dt, int64_t lddz, int64_t rows, int6
                         const void* gamma, const void* beta, int wdt, void* dW, int odt,
                         int64_t ldw, int B, float* db, void* ws, size_t ws_bytes, void* stream);
 dash_status dash_weight_grad_workspace_size(int64_t rows, int64_t outs, int64_t cols, int dt,
-                                            int B, size_t* bytes);
+                                            int64_t lddz, int B, size_t* bytes);
 
 /* Workspace bytes for op on N blocks of order B (param: iters for CN/NDB,
  * degree for Chebyshev, n_vec for spectral_scale; gdt for accumulate/apply is

@@ -134,7 +134,8 @@ def load_library(path=None):
     lib.dash_layer_norm_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     lib.weight_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, vp, vp, i32, vp, i32,
                                 i64, i32, vp, vp, sz, vp]
-    lib.dash_weight_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(sz)]
+    lib.dash_weight_grad_workspace_size.argtypes = [i64, i64, i64, i32, i64, i32,
+                                                    ctypes.POINTER(sz)]
     lib.dash_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp]
     lib.dash_workspace_size.argtypes = [i32, i64, i32, i32, i32, ctypes.POINTER(sz)]
     lib.dash_op_matmuls.argtypes = [i32, i32]
@@ -804,10 +805,12 @@ def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=N
     return dx, dgamma, dbeta
 
 
-def weight_grad_workspace_size(rows, outs, cols, dtype=torch.bfloat16, B=None):
+def weight_grad_workspace_size(rows, outs, cols, dtype=torch.bfloat16, B=None, lddz=0):
+    """Workspace bytes of weight_grad.  lddz: the row stride of a dz whose address is a
+    multiple of 16 bytes; 0 covers any dz."""
     out = ctypes.c_size_t(0)
     _check(load_library().dash_weight_grad_workspace_size(
-        int(rows), int(outs), int(cols), _DTYPES.get(dtype, -1), int(B or 0), ctypes.byref(out)),
+        rows, outs, cols, _DTYPES.get(dtype, -1), lddz, int(B or 0), ctypes.byref(out)),
         "dash_weight_grad_workspace_size")
     return out.value
 
@@ -841,7 +844,8 @@ def weight_grad(dz, q, scale, cols, fmt="int8", gamma=None, beta=None, B=None, d
         ldw, _ = _rows(out, "out", None, (outs, cols))
     db = torch.empty(outs, dtype=torch.float32, device=dev) if bias else None
     if ws is None:
-        ws = torch.empty(max(weight_grad_workspace_size(rows, outs, cols, dz.dtype, b), 256),
+        ld = 0 if dz.data_ptr() & 15 else lddz
+        ws = torch.empty(max(weight_grad_workspace_size(rows, outs, cols, dz.dtype, b, ld), 256),
                          dtype=torch.uint8, device=dev)
     _check(lib.weight_grad(dz.data_ptr(), dt, lddz, rows, outs, q.data_ptr(), scale.data_ptr(), f,
                            cols, _addr(gamma), _addr(beta), wdt, out.data_ptr(), _gdt(out), ldw, b,

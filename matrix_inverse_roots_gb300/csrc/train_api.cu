@@ -32,6 +32,13 @@ bool valid_codes(const uint8_t* q, const uint8_t* scale) {
   return q != nullptr && scale != nullptr && aligned(q, 16);
 }
 
+// Sizes of a weight gradient; dW of 2^44 elements and more is beyond any memory and the
+// tile count's type.
+bool valid_weight(int64_t rows, int64_t outs, int64_t cols, int B) {
+  return valid_sizes(rows, cols) && valid_sizes(rows, outs) && outs * cols < (int64_t{1} << 44) &&
+         (B == 0 || (B >= 128 && B <= 2048 && B % 128 == 0));
+}
+
 }  // namespace
 
 extern "C" {
@@ -117,12 +124,12 @@ dash_status layer_norm_backward(const void* dy, int64_t lddy, int dt, int64_t ro
 }
 
 dash_status dash_weight_grad_workspace_size(int64_t rows, int64_t outs, int64_t cols, int dt,
-                                            int B, size_t* bytes) {
-  if (bytes == nullptr || !valid_sizes(rows, cols) || !valid_sizes(rows, outs) || !valid_dt(dt) ||
-      (B != 0 && (B < 128 || B > 2048 || B % 128 != 0)))
+                                            int64_t lddz, int B, size_t* bytes) {
+  if (bytes == nullptr || !valid_weight(rows, outs, cols, B) || !valid_dt(dt) || lddz < 0)
     return DASH_ERR_INVALID_ARG;
   WeightGradArgs a = {};
   a.dt = dt;
+  a.lddz = lddz;
   a.rows = rows;
   a.outs = outs;
   a.cols = cols;
@@ -136,11 +143,10 @@ dash_status weight_grad(const void* dz, int dt, int64_t lddz, int64_t rows, int6
                         const void* gamma, const void* beta, int wdt, void* dW, int odt,
                         int64_t ldw, int B, float* db, void* ws, size_t ws_bytes, void* stream) {
   if (!valid_dt(dt) || !valid_dt(wdt) || !valid_dt(odt) || !valid_fmt(fmt) ||
-      !valid_sizes(rows, cols) || !valid_sizes(rows, outs) ||
-      (B != 0 && (B < 128 || B > 2048 || B % 128 != 0)))
+      !valid_weight(rows, outs, cols, B))
     return DASH_ERR_INVALID_ARG;
   if (outs == 0 || cols == 0) return DASH_OK;
-  if (dW == nullptr || !aligned(dW, dt_bytes(odt)) || (B == 0 && ldw < cols) ||
+  if (dW == nullptr || !aligned(dW, B ? 16 : dt_bytes(odt)) || (B == 0 && ldw < cols) ||
       !optional_vector(gamma, wdt) || !optional_vector(beta, wdt) || !aligned(db, 4))
     return DASH_ERR_INVALID_ARG;
   if (rows > 0 && (!valid_matrix(dz, dt, outs, lddz) || !valid_codes(q, scale)))

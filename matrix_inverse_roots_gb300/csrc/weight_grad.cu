@@ -2,113 +2,845 @@
 //   dW[o][i] = gamma[i] sum_t dz[t][o] n[t][i] + beta[i] db[o],   db[o] = sum_t dz[t][o],
 // n the checkpoint's values, written as a matrix or as the B x B blocks of
 // shampoo_accumulate.
+//
+// The product over tokens runs on the tensor cores in bf16.  Neither operand is rounded:
+// a checkpoint's value (7 or 4 bits times a power of two) is a bf16 number, and dz enters
+// as bf16 parts that add up to it (one for bf16, two for fp16, three for fp32).  gamma
+// and beta belong to columns of dW, so they are applied to the sums.
+//
+// Design (persistent, CTA pairs on 256 x 256 tiles of dW, cta_group::2; both operands lie
+// in memory with the token index outermost, so both are MN-major):
+//   warp 0       TMA producer of A: 128 columns of dz per CTA, 64 tokens per slot.
+//   warp 2       TMA producer of the codes: 128 columns, 64 tokens (8 KB) per slot.
+//   warps 4-11   converters: codes and scales (scales straight from global memory, two
+//                slots ahead) to bf16, into the 128-byte-swizzled layout the MMA reads.
+//   warp 3       hands a converted slot to the leader CTA: the converters' arrivals stay
+//                inside the CTA, and this one thread, which has no memory traffic of its
+//                own to wait for, makes the cluster-scope release.
+//   warp 1       of the leader issues the MMAs into one of two TMEM accumulators.
+//   warps 12-15  epilogue of the previous tile.
+// Tiles that do not fill a whole round of the pairs are split along the tokens; their
+// fp32 partial sums are joined, in order, by a second kernel.
+// Every wait is bounded (see mbar_wait); a time-out sets the device error flag, and the
+// CTA drains its copies and MMAs, frees TMEM and returns.
+#include <mutex>
+
 #include "act_q8.cuh"
 #include "dash_internal.h"
 #include "train_internal.h"
 
 namespace dash {
 
-constexpr int WG_TILE = 64, WG_K = 16;
+int weight_grad_read_clear_error() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_dash_error, sizeof(int)) != cudaSuccess) return -1;
+  if (cudaMemcpyToSymbol(g_dash_error, &z, sizeof(int)) != cudaSuccess) return -1;
+  return v;
+}
 
-// One CTA per 64 x 64 tile, 4 x 4 outputs per thread, fp32 arithmetic.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(256) weight_grad_kernel(const WeightGradArgs a, const float* db) {
-  __shared__ float sa[WG_K][WG_TILE + 4], sb[WG_K][WG_TILE + 4];
-  const long long ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP;
-  const long long o0 = static_cast<long long>(blockIdx.y) * WG_TILE;
-  const long long i0 = static_cast<long long>(blockIdx.x) * WG_TILE;
-  const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (long long t0 = 0; t0 < a.rows; t0 += WG_K) {
-    for (int e = threadIdx.x; e < WG_K * WG_TILE; e += 256) {
-      const int k = e / WG_TILE, j = e % WG_TILE;
-      const long long t = t0 + k;
-      float va = 0.0f, vb = 0.0f;
-      if (t < a.rows) {
-        if (o0 + j < a.outs) va = Elem<T>::to(static_cast<const T*>(a.dz)[t * a.lddz + o0 + j]);
-        if (i0 + j < a.cols)
-          vb = q8_value<FMT>(a.q[t * ng * Q8_GROUP + i0 + j]) *
-               q8_scale(a.scale[t * ng + (i0 + j) / Q8_GROUP]);
-      }
-      sa[k][j] = va;
-      sb[k][j] = vb;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < WG_K; ++k)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          acc[u][v] = fmaf(sa[k][tr * 4 + u], sb[k][tc * 4 + v], acc[u][v]);
-    __syncthreads();
+namespace {
+
+constexpr int WT = 256;              // tile of dW per CTA pair (both directions)
+constexpr int WK = 64;               // tokens per slot
+constexpr int WA_BYTES = 128 * WK * 2;  // A slot: 128 columns of dz, two 64-column boxes
+constexpr int WB_BYTES = 128 * WK * 2;  // converted B slot: 128 columns, two boxes
+constexpr int WQ_BYTES = 128 * WK;      // codes slot
+constexpr int W_BOX = WK * 128;         // one 64-column box of bf16: 64 rows of 128 B
+constexpr int NA = 5, NB = 5, NQ = 5;
+constexpr int W_CONV = 8, W_EPI = 4;    // converter and epilogue warps
+constexpr int W_THREADS = 32 * (4 + W_CONV + W_EPI);
+constexpr int W_BARS = 2 * NA + 2 * NQ + 3 * NB + 4 + 1;
+constexpr int W_SMEM = NA * WA_BYTES + NB * WB_BYTES + NQ * WQ_BYTES + 1024 + 512;
+static_assert(W_SMEM <= 232448, "shared memory budget");
+static_assert(8 * W_BARS + 16 <= 512, "barrier area");
+
+struct WParams {
+  int nkb;             // slots of 64 tokens
+  int parts;           // bf16 parts of dz
+  int tiles_m, tiles_n;
+  int full;            // tiles computed whole
+  int split, kper;     // the others: `split` units of kper slots each
+  int units;
+  long long rows, ng;
+  const uint8_t* scale;
+  const float* db;     // column sums of dz (null without beta)
+  float* partial;      // (units - full) x 256 x 256 sums
+  WeightGradArgs a;
+};
+
+// Tile t of the raster: groups of 8 tile rows, walked column by column, so that the tiles
+// in flight share few panels of both operands.
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& mt, int& nt) {
+  constexpr int G = 8;
+  const int per = G * tiles_n;
+  const int g = t / per;
+  const int h = tiles_m - g * G < G ? tiles_m - g * G : G;
+  const int r = t - g * per;
+  mt = g * G + r % h;
+  nt = r / h;
+}
+
+struct Unit {
+  int mt, nt, k0, k1, part;  // part: index of the partial tile, -1 for a whole one
+};
+
+__device__ __forceinline__ Unit unit_at(int u, const WParams& p) {
+  Unit x;
+  int t = u;
+  x.part = -1;
+  x.k0 = 0;
+  x.k1 = p.nkb;
+  if (u >= p.full) {
+    x.part = u - p.full;
+    t = p.full + x.part / p.split;
+    x.k0 = (x.part % p.split) * p.kper;
+    x.k1 = x.k0 + p.kper < p.nkb ? x.k0 + p.kper : p.nkb;
   }
-  const long long pr = a.block ? (a.outs + a.block - 1) / a.block * a.block : a.outs;
-  const long long pc = a.block ? (a.cols + a.block - 1) / a.block * a.block : a.cols;
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const long long o = o0 + tr * 4 + u, i = i0 + tc * 4 + v;
-      if (o >= pr || i >= pc) continue;
-      float d = 0.0f;
-      if (o < a.outs && i < a.cols) {
-        d = acc[u][v];
-        if (a.gamma) d *= load_dt(a.gamma, a.wdt, i);
-        if (a.beta) d = fmaf(db[o], load_dt(a.beta, a.wdt, i), d);
+  tile_at(t, p.tiles_m, p.tiles_n, x.mt, x.nt);
+  return x;
+}
+
+// Where element (o, i) of dW is stored.
+__device__ __forceinline__ long long dw_index(const WeightGradArgs& a, long long o, long long i) {
+  if (a.block == 0) return o * a.ldw + i;
+  const long long b = a.block, nbc = (a.cols + b - 1) / b;
+  return ((o / b) * nbc + i / b) * b * b + (o % b) * b + i % b;
+}
+__host__ __device__ __forceinline__ long long padded(long long n, int b) {
+  return b ? (n + b - 1) / b * b : n;
+}
+
+__device__ __forceinline__ void store_dt(void* p, int dt, long long i, float v) {
+  if (dt == DASH_DT_F32)
+    static_cast<float*>(p)[i] = v;
+  else if (dt == DASH_DT_BF16)
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Scales W consecutive sums of row o from column i on and stores them (W a power of two
+// that divides i; a block's rows hold whole groups of W).  Outside the valid part a block
+// is zero, whatever the sums there (a NaN code meets a zero there).
+template <int W>
+__device__ __forceinline__ void finish_store(const WeightGradArgs& a, const float* db, long long o,
+                                             long long i, float (&v)[W]) {
+  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+  if (o >= pr || i >= pc) return;
+  const float dbo = (db != nullptr && o < a.outs) ? db[o] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    if (o < a.outs && i + j < a.cols) {
+      if (a.gamma) v[j] *= load_dt(a.gamma, a.wdt, i + j);
+      if (a.beta) v[j] = fmaf(dbo, load_dt(a.beta, a.wdt, i + j), v[j]);
+    } else {
+      v[j] = 0.0f;
+    }
+  }
+  const long long at = dw_index(a, o, i);
+  if (i + W <= pc) {
+    if (a.odt == DASH_DT_F32) {
+      float* p = static_cast<float*>(a.dw) + at;
+      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+        for (int j = 0; j < W; j += 4)
+          *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        return;
       }
-      long long at = o * a.ldw + i;
-      if (a.block) {
-        const long long b = a.block;
-        at = ((o / b) * (pc / b) + i / b) * b * b + (o % b) * b + i % b;
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(a.dw) + at;
+      if ((reinterpret_cast<uintptr_t>(p) & (W * 2 < 16 ? W * 2 - 1 : 15u)) == 0) {
+        uint32_t r[W / 2];
+#pragma unroll
+        for (int j = 0; j < W / 2; ++j)
+          r[j] = a.odt == DASH_DT_BF16 ? pack_bf162(v[2 * j], v[2 * j + 1])
+                                       : pack_half2(v[2 * j], v[2 * j + 1]);
+        if constexpr (W >= 8) {
+#pragma unroll
+          for (int j = 0; j < W / 8; ++j)
+            reinterpret_cast<uint4*>(p)[j] =
+                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+        } else {
+          *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+        }
+        return;
       }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+    if (i + j < pc) store_dt(a.dw, a.odt, at + j, v[j]);
+}
+
+// 16 codes (one 16-byte word of a row) to 16 bf16 numbers, two 16-byte words.
+template <int FMT>
+__device__ __forceinline__ void convert16(const uint4& c, float s, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float f[4];
+    if (FMT == DASH_Q8_INT8) {
+      // 2^23 + (q + 128) from the code's byte, less 2^23 + 128, times 2^e: all exact.
+      const uint32_t u = w[j] ^ 0x80808080u;
+      f[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.0f;
+      f[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.0f;
+      f[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.0f;
+      f[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.0f;
+    } else {
+      // The code's exponent and mantissa as an fp32 number's, 2^120 too small.
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t b = w[j] >> (8 * k);
+        f[k] = __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7fu) << 20)) * 0x1p120f;
+      }
+    }
+    // The products are bf16 numbers: their upper halves are all of them.
+    r[2 * j] = __byte_perm(__float_as_uint(f[0] * s), __float_as_uint(f[1] * s), 0x7632);
+    r[2 * j + 1] = __byte_perm(__float_as_uint(f[2] * s), __float_as_uint(f[3] * s), 0x7632);
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(W_THREADS, 1)
+    weight_grad_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tQ,
+                       const __grid_constant__ WParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw_base + pad;
+  constexpr int OFF_B = NA * WA_BYTES;
+  constexpr int OFF_Q = OFF_B + NB * WB_BYTES;
+  constexpr int OFF_BAR = OFF_Q + NQ * WQ_BYTES;
+  const uint32_t bar0 = sbase + OFF_BAR;
+  auto afull = [&](int s) { return bar0 + 8u * s; };
+  auto aempty = [&](int s) { return bar0 + 8u * (NA + s); };
+  auto qfull = [&](int s) { return bar0 + 8u * (2 * NA + s); };
+  auto qempty = [&](int s) { return bar0 + 8u * (2 * NA + NQ + s); };
+  auto bconv = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + s); };
+  auto bfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + NB + s); };
+  auto bempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 2 * NB + s); };
+  auto tfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 3 * NB + s); };
+  auto tempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 3 * NB + 2 + s); };
+  const uint32_t fin_bar = bar0 + 8u * (W_BARS - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8 * W_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * W_BARS + 8);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const bool leader = (crank == 0);
+  const int cid = blockIdx.x / 2;
+  const int ncl = gridDim.x / 2;
+  constexpr uint16_t kMask = 3;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NA; ++s) {
+      mbar_init(afull(s), 1);
+      mbar_init(aempty(s), 1);
+    }
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(qfull(s), 1);
+      mbar_init(qempty(s), W_CONV);
+    }
+    for (int s = 0; s < NB; ++s) {
+      mbar_init(bconv(s), W_CONV);
+      mbar_init(bfull(s), 2);  // warp 3 of both CTAs
+      mbar_init(bempty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(tfull(s), 1);
+      mbar_init(tempty(s), 2 * W_EPI);
+    }
+    mbar_init(fin_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tA);
+    tma_prefetch_desc(&tQ);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------- A producer
+      int s = 0;
+      uint32_t ph = 0, armed = 0, armed_par = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < p.units; u += ncl) {
+        const Unit x = unit_at(u, p);
+        const int o0 = x.mt * WT + static_cast<int>(crank) * 128;
+        for (int kb = x.k0; ok && kb < x.k1; ++kb) {
+          for (int part = 0; part < p.parts; ++part) {
+            if (!mbar_wait(aempty(s), ph ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            uint32_t fb = afull(s);
+            if (leader) {
+              mbar_arrive_expect_tx(fb, 2 * WA_BYTES);
+              armed |= 1u << s;
+              armed_par = (armed_par & ~(1u << s)) | (ph << s);
+            } else {
+              fb = mapa_shared(fb, 0);
+            }
+            const uint32_t dst = sbase + s * WA_BYTES;
+            tma_load_3d_pair(dst, &tA, fb, o0, kb * WK, part);
+            tma_load_3d_pair(dst + W_BOX, &tA, fb, o0 + 64, kb * WK, part);
+            if (++s == NA) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
+      if (!ok)
+        for (int i = 0; i < NA; ++i)
+          if (armed & (1u << i)) mbar_wait_drain(afull(i), (armed_par >> i) & 1u);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      // -------------------------------------------------------- codes producer
+      int s = 0;
+      uint32_t ph = 0, armed = 0, armed_par = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < p.units; u += ncl) {
+        const Unit x = unit_at(u, p);
+        const int i0 = x.nt * WT + static_cast<int>(crank) * 128;
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          if (!mbar_wait(qempty(s), ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(qfull(s), WQ_BYTES);
+          armed |= 1u << s;
+          armed_par = (armed_par & ~(1u << s)) | (ph << s);
+          tma_load_3d(sbase + OFF_Q + s * WQ_BYTES, &tQ, qfull(s), i0, kb * WK, 0);
+          if (++s == NQ) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok)
+        for (int i = 0; i < NQ; ++i)
+          if (armed & (1u << i)) mbar_wait_drain(qfull(i), (armed_par >> i) & 1u);
+    }
+  } else if (warp == 3) {
+    if (lane == 0) {
+      // -------------------------------------------------------- hand-over of B slots
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < p.units; u += ncl) {
+        const Unit x = unit_at(u, p);
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          if (!mbar_wait(bconv(s), ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_cluster(mapa_shared(bfull(s), 0));
+          if (++s == NB) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // -------------------------------------------------------- MMA issuer
+      const uint32_t idesc = make_idesc(1, 1, 1, 256, 256);
+      int sa = 0, sb = 0, acc = 0;
+      uint32_t pa = 0, pb = 0, pacc = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < p.units; u += ncl) {
+        const Unit x = unit_at(u, p);
+        if (!mbar_wait(tempty(acc), pacc ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * WT);
+        for (int kb = x.k0; ok && kb < x.k1; ++kb) {
+          if (!mbar_wait_cluster(bfull(sb), pb, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sB = sbase + OFF_B + sb * WB_BYTES;
+          for (int part = 0; part < p.parts; ++part) {
+            if (!mbar_wait(afull(sa), pa, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sA = sbase + sa * WA_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < WK / 16; ++kk)
+              mma_f16_pair(d, smem_desc(sA + kk * 16 * 128, W_BOX, 1024, LAYOUT_SW128),
+                           smem_desc(sB + kk * 16 * 128, W_BOX, 1024, LAYOUT_SW128), idesc,
+                           (kb > x.k0 || part > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_pair_mc(aempty(sa), kMask);
+            if (++sa == NA) {
+              sa = 0;
+              pa ^= 1u;
+            }
+          }
+          if (!ok) break;
+          mma_commit_pair_mc(bempty(sb), kMask);
+          if (++sb == NB) {
+            sb = 0;
+            pb ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_mc(tfull(acc), kMask);
+        acc ^= 1;
+        if (acc == 0) pacc ^= 1u;
+      }
+      // Every MMA issued above must be complete before TMEM is released.
+      mma_commit_pair(fin_bar);
+      mbar_wait_drain(fin_bar, 0);
+    }
+  } else if (warp < 4 + W_CONV) {
+    // ---------------------------------------------------------- converters
+    // Thread c of 256: row t = c / 8 (and t + 32) of the slot, 16 columns from 16 (c % 8).
+    const int c = threadIdx.x - 128;
+    const int t = c >> 3, c16 = c & 7;
+    int sq = 0, sb = 0;
+    uint32_t pq = 0, pb = 0;
+    bool ok = true;
+    for (int u = cid; ok && u < p.units; u += ncl) {
+      const Unit x = unit_at(u, p);
+      const long long g = x.nt * (WT / Q8_GROUP) + static_cast<int>(crank) * 4 + (c16 >> 1);
+      const bool gin = g < p.ng;
+      // Scale bytes of this thread's two rows of slot kb; 0 (a scale of 0) outside.
+      auto scales = [&](int kb) -> uint32_t {
+        uint32_t v = 0;
+        const long long r = static_cast<long long>(kb) * WK + t;
+        if (gin && kb < x.k1) {
+          if (r < p.rows) v = p.scale[r * p.ng + g];
+          if (r + 32 < p.rows) v |= static_cast<uint32_t>(p.scale[(r + 32) * p.ng + g]) << 8;
+        }
+        return v;
+      };
+      uint32_t v0 = scales(x.k0), v1 = scales(x.k0 + 1);
+      for (int kb = x.k0; kb < x.k1; ++kb) {
+        const uint32_t v2 = scales(kb + 2);
+        if (!mbar_wait(qfull(sq), pq, abort_flag) || !mbar_wait(bempty(sb), pb ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = smem + OFF_Q + sq * WQ_BYTES + c16 * 16;
+        const uint4 q0 = *reinterpret_cast<const uint4*>(src + t * 128);
+        const uint4 q1 = *reinterpret_cast<const uint4*>(src + (t + 32) * 128);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty(sq));
+        uint8_t* box = smem + OFF_B + sb * WB_BYTES + (c16 >> 2) * W_BOX;
+        // 16-byte words 2 (c16 % 4) and + 1 of the row, at the swizzled places; the upper
+        // box's threads write the odd word first, so that a row's eight threads hit all
+        // banks once.
+        const int w = (c16 & 3) * 2, odd = c16 >> 2, sw = t & 7;
+        uint8_t* r0 = box + t * 128;
+        uint4 lo, hi;
+        convert16<FMT>(q0, q8_scale(v0 & 0xffu), lo, hi);
+        *reinterpret_cast<uint4*>(r0 + (((w + odd) ^ sw) << 4)) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(r0 + (((w + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+        r0 += 32 * 128;  // (t + 32) % 8 == t % 8
+        convert16<FMT>(q1, q8_scale(v0 >> 8), lo, hi);
+        *reinterpret_cast<uint4*>(r0 + (((w + odd) ^ sw) << 4)) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(r0 + (((w + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bconv(sb));
+        v0 = v1;
+        v1 = v2;
+        if (++sq == NQ) {
+          sq = 0;
+          pq ^= 1u;
+        }
+        if (++sb == NB) {
+          sb = 0;
+          pb ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3;  // TMEM lane quarter
+    int acc = 0;
+    uint32_t pacc = 0;
+    for (int u = cid; u < p.units; u += ncl) {
+      const Unit x = unit_at(u, p);
+      if (!mbar_wait(tfull(acc), pacc, abort_flag)) break;
+      tc_fence_after();
+      const int row = static_cast<int>(crank) * 128 + q * 32 + lane;  // in the tile
+      const uint32_t taddr =
+          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * WT);
+#pragma unroll 1
+      for (int cc = 0; cc < WT / 16; ++cc) {
+        uint32_t r[16];
+        tmem_ld16(taddr + cc * 16, r);
+        tmem_wait_ld(r);
+        if (cc + 1 == WT / 16) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+        }
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+        if (x.part >= 0) {
+          float4* d = reinterpret_cast<float4*>(
+              p.partial + (static_cast<long long>(x.part) * WT + row) * WT + cc * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+          finish_store<16>(p.a, p.db, static_cast<long long>(x.mt) * WT + row,
+                           static_cast<long long>(x.nt) * WT + cc * 16, v);
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) pacc ^= 1u;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // No CTA may leave while a peer can still signal into it or use its TMEM.
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// Joins the partial sums of the tiles split along the tokens (none at all for split 0, a
+// gradient over no tokens).  A warp per 128 columns of a tile's row.
+__global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_constant__ WParams p,
+                                                               int first, int ntiles) {
+  const long long total = static_cast<long long>(ntiles) * WT * (WT / 4);
+  for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < total;
+       e += static_cast<long long>(gridDim.x) * 256) {
+    const int c4 = static_cast<int>(e % (WT / 4));
+    const long long rr = e / (WT / 4);
+    const int row = static_cast<int>(rr % WT);
+    const int t = static_cast<int>(rr / WT);
+    int mt, nt;
+    tile_at(first + t, p.tiles_m, p.tiles_n, mt, nt);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < p.split; ++s) {
+      const float4 f = *reinterpret_cast<const float4*>(
+          p.partial + ((static_cast<long long>(t) * p.split + s) * WT + row) * WT + c4 * 4);
+      v[0] += f.x;
+      v[1] += f.y;
+      v[2] += f.z;
+      v[3] += f.w;
+    }
+    finish_store<4>(p.a, p.db, static_cast<long long>(mt) * WT + row,
+                    static_cast<long long>(nt) * WT + c4 * 4, v);
+  }
+}
+
+// Zeros in the blocks' padding that no tile reaches: rows from r0 on, and columns from c0.
+__global__ void __launch_bounds__(256)
+    weight_grad_pad_kernel(const WeightGradArgs a, long long r0, long long c0) {
+  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+  for (long long o = blockIdx.y; o < pr; o += gridDim.y) {
+    const long long from = o < r0 ? c0 : 0;
+    for (long long i = from + (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4; i < pc;
+         i += static_cast<long long>(gridDim.x) * 1024) {
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const long long at = dw_index(a, o, i);
       if (a.odt == DASH_DT_F32)
-        static_cast<float*>(a.dw)[at] = d;
-      else if (a.odt == DASH_DT_BF16)
-        static_cast<__nv_bfloat16*>(a.dw)[at] = __float2bfloat16_rn(d);
+        *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at) =
+            make_float4(v[0], v[1], v[2], v[3]);
       else
-        static_cast<__half*>(a.dw)[at] = __float2half_rn(d);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at) = make_uint2(0u, 0u);
+    }
+  }
+}
+
+// dz as bf16 parts that add up to it, (parts, rows, ldp).  Every part but the last keeps
+// the upper bits (truncated, so that no part overflows); what is left is exact.
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(256)
+    split_kernel(const T* dz, long long rows, long long outs, long long ld, long long ldp,
+                 uint16_t* out) {
+  for (long long r = blockIdx.y; r < rows; r += gridDim.y)
+    for (long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; c < outs;
+         c += static_cast<long long>(gridDim.x) * 256) {
+      float v = Elem<T>::to(dz[r * ld + c]);
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) {
+        const uint32_t b = __float_as_uint(v) & 0xffff0000u;
+        uint32_t h = b >> 16;
+        // Non-finite: the first part carries it (a NaN keeps a mantissa bit), the others
+        // are zero.
+        if ((b & 0x7f800000u) == 0x7f800000u) {
+          if (v != v) h = 0x7fc0u;
+          v = 0.0f;
+        } else {
+          v -= __uint_as_float(b);
+        }
+        out[(k * rows + r) * ldp + c] = static_cast<uint16_t>(h);
+      }
     }
 }
 
-static size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Workspace: db (when only beta needs it), then the column sums' partials.
-size_t weight_grad_ws(const WeightGradArgs& a) {
-  const size_t outs = static_cast<size_t>(a.outs);
-  return round256(outs * 4) + round256(outs * 4 * col_sum_parts(a.rows, a.outs));
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, []() {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(ptr);
+  });
+  return fn;
 }
 
-template <typename T>
-static dash_status weight_grad_t(const WeightGradArgs& a, const float* db, cudaStream_t st) {
-  const long long b = a.block;
-  const long long pr = b ? (a.outs + b - 1) / b * b : a.outs;
-  const long long pc = b ? (a.cols + b - 1) / b * b : a.cols;
-  const dim3 grid(static_cast<unsigned>((pc + WG_TILE - 1) / WG_TILE),
-                  static_cast<unsigned>((pr + WG_TILE - 1) / WG_TILE));
-  if (a.fmt == DASH_Q8_INT8)
-    weight_grad_kernel<T, DASH_Q8_INT8><<<grid, 256, 0, st>>>(a, db);
-  else
-    weight_grad_kernel<T, DASH_Q8_E4M3><<<grid, 256, 0, st>>>(a, db);
-  return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+// (inner, rows, planes) with the given row and plane strides in bytes.
+bool make_map(CUtensorMap* m, const void* base, bool bytes, uint64_t inner, uint64_t rows,
+              uint64_t planes, uint64_t row_bytes, uint64_t plane_bytes, uint32_t box_inner,
+              uint32_t box_rows, bool swizzle) {
+  EncodeFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dim[3] = {inner, rows, planes};
+  cuuint64_t stride[2] = {row_bytes, plane_bytes};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+             const_cast<void*>(base), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs that can be resident at once, per device; 0 on error.
+int resident_pairs() {
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cache[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(512, 1, 1);
+    cfg.blockDim = dim3(W_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = W_SMEM;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    for (auto k : {weight_grad_kernel<DASH_Q8_INT8>, weight_grad_kernel<DASH_Q8_E4M3>})
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM) !=
+          cudaSuccess)
+        return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, weight_grad_kernel<DASH_Q8_INT8>, &cfg) != cudaSuccess)
+      return 0;
+    const int sms = device_sm_count() / 2;
+    cache[dev] = n < sms ? n : sms;
+  }
+  return cache[dev];
+}
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// How the tiles are shared out among P pairs: whole tiles for as many full rounds as
+// there are, the rest split along the tokens.  A split into S costs ceil(tail S / P)
+// rounds of nkb / S slots; its partial tiles are written and read back once (about 0.1 us
+// each when every pair does so) and a second launch joins them.  In units of one slot's
+// 4 MMAs, about 0.3 us.
+struct Plan {
+  int tiles_m, tiles_n, nkb, parts, full, split, kper, units;
+};
+
+Plan make_plan(const WeightGradArgs& a, int pairs) {
+  Plan p;
+  p.tiles_m = static_cast<int>((a.outs + WT - 1) / WT);
+  p.tiles_n = static_cast<int>((a.cols + WT - 1) / WT);
+  p.nkb = static_cast<int>((a.rows + WK - 1) / WK);
+  p.parts = a.dt == DASH_DT_F32 ? 3 : (a.dt == DASH_DT_F16 ? 2 : 1);
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int tail = tiles % pairs;
+  p.full = tiles;
+  p.split = 1;
+  p.kper = p.nkb;
+  double best = tail ? static_cast<double>(p.nkb) * p.parts : 0.0;
+  const int most = p.nkb / 4 < 64 ? p.nkb / 4 : 64;
+  for (int s = 2; tail && s <= most; ++s) {
+    const int kper = (p.nkb + s - 1) / s;
+    const int se = (p.nkb + kper - 1) / kper;
+    if (se < 2) continue;
+    const double cost = static_cast<double>((tail * se + pairs - 1) / pairs) * kper * p.parts +
+                        12.0 + 0.3 * tail * se;
+    if (cost < best) {
+      best = cost;
+      p.full = tiles - tail;
+      p.split = se;
+      p.kper = kper;
+    }
+  }
+  p.units = p.full + (p.split > 1 ? tail * p.split : 0);
+  return p;
+}
+
+// Whether TMA can read dz where it lies.
+bool dz_direct(const WeightGradArgs& a) {
+  return a.dt == DASH_DT_BF16 && (reinterpret_cast<uintptr_t>(a.dz) & 15u) == 0 &&
+         a.lddz % 8 == 0 && a.lddz > 0;
+}
+
+long long part_ld(const WeightGradArgs& a) { return (a.outs + 7) / 8 * 8; }
+
+template <typename T, int PARTS>
+cudaError_t run_split(const WeightGradArgs& a, uint16_t* out, cudaStream_t st) {
+  const long long gx = (a.outs + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(gx < 64 ? gx : 64),
+                  static_cast<unsigned>(a.rows < 65535 ? a.rows : 65535));
+  split_kernel<T, PARTS><<<grid, 256, 0, st>>>(static_cast<const T*>(a.dz), a.rows, a.outs,
+                                               a.lddz, part_ld(a), out);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Workspace: db (when only beta needs it), the column sums' partials, dz's parts, the
+// partial tiles.  Without a device (sizes asked for on the host alone) the most partial
+// tiles any number of pairs can need.
+static size_t carve(const WeightGradArgs& a, const Plan& p, size_t& o_part, size_t& o_dz,
+                    size_t& o_tiles) {
+  size_t n = round256(static_cast<size_t>(a.outs) * 4);
+  o_part = n;
+  n += round256(static_cast<size_t>(a.outs) * 4 * col_sum_parts(a.rows, a.outs));
+  o_dz = n;
+  if (!dz_direct(a))
+    n += round256(static_cast<size_t>(p.parts) * a.rows * part_ld(a) * 2);
+  o_tiles = n;
+  n += static_cast<size_t>(p.units - p.full) * WT * WT * 4;
+  return n;
+}
+
+size_t weight_grad_ws(const WeightGradArgs& a) {
+  const int pairs = resident_pairs();
+  size_t x, y, z;
+  return carve(a, make_plan(a, pairs > 0 ? pairs : 76), x, y, z);
 }
 
 dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t st) {
+  const int pairs = resident_pairs();
+  if (pairs <= 0) return DASH_ERR_CUDA;
+  const Plan plan = make_plan(a, pairs);
+  size_t o_part, o_dz, o_tiles;
+  carve(a, plan, o_part, o_dz, o_tiles);
+  uint8_t* w = static_cast<uint8_t*>(ws);
   float* db = a.db;
   if (a.db || a.beta) {
-    if (!db) db = static_cast<float*>(ws);
-    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                           round256(static_cast<size_t>(a.outs) * 4));
-    const dash_status s = launch_col_sum(a.dz, a.dt, a.rows, a.outs, a.lddz, part, db, st);
+    if (!db) db = reinterpret_cast<float*>(w);
+    const dash_status s = launch_col_sum(a.dz, a.dt, a.rows, a.outs, a.lddz,
+                                         reinterpret_cast<float*>(w + o_part), db, st);
     if (s != DASH_OK) return s;
   }
   const int rec = trace_begin(st);
-  const dash_status s = a.dt == DASH_DT_F32    ? weight_grad_t<float>(a, db, st)
-                        : a.dt == DASH_DT_BF16 ? weight_grad_t<__nv_bfloat16>(a, db, st)
-                                               : weight_grad_t<__half>(a, db, st);
+  cudaError_t err = cudaSuccess;
+  WParams p = {};
+  p.nkb = plan.nkb;
+  p.parts = plan.parts;
+  p.tiles_m = plan.tiles_m;
+  p.tiles_n = plan.tiles_n;
+  p.full = plan.full;
+  p.split = plan.split;
+  p.kper = plan.kper;
+  p.units = plan.units;
+  p.rows = a.rows;
+  p.ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP;
+  p.scale = a.scale;
+  p.db = a.beta ? db : nullptr;
+  p.partial = reinterpret_cast<float*>(w + o_tiles);
+  p.a = a;
+  if (a.rows > 0) {
+    const void* dz = a.dz;
+    uint64_t row_bytes = static_cast<uint64_t>(a.lddz) * 2, plane_bytes = row_bytes * a.rows;
+    if (!dz_direct(a)) {
+      uint16_t* out = reinterpret_cast<uint16_t*>(w + o_dz);
+      if (a.dt == DASH_DT_F32)
+        err = run_split<float, 3>(a, out, st);
+      else if (a.dt == DASH_DT_F16)
+        err = run_split<__half, 2>(a, out, st);
+      else
+        err = run_split<__nv_bfloat16, 1>(a, out, st);
+      dz = out;
+      row_bytes = static_cast<uint64_t>(part_ld(a)) * 2;
+      plane_bytes = row_bytes * a.rows;
+    }
+    CUtensorMap tA, tQ;
+    if (err != cudaSuccess ||
+        !make_map(&tA, dz, false, a.outs, a.rows, plan.parts, row_bytes, plane_bytes, 64, WK,
+                  true) ||
+        !make_map(&tQ, a.q, true, p.ng * Q8_GROUP, a.rows, 1, p.ng * Q8_GROUP,
+                  static_cast<uint64_t>(p.ng) * Q8_GROUP * a.rows, 128, WK, false)) {
+      trace_end(rec, st, DASH_TRACE_GEMM_BF16, 0.0, 0.0);
+      return DASH_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (plan.units < pairs ? plan.units : pairs)), 1, 1);
+    cfg.blockDim = dim3(W_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = W_SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto k = a.fmt == DASH_Q8_INT8 ? weight_grad_kernel<DASH_Q8_INT8>
+                                   : weight_grad_kernel<DASH_Q8_E4M3>;
+    err = cudaLaunchKernelEx(&cfg, k, tA, tQ, p);
+  }
+  const int tiles = plan.tiles_m * plan.tiles_n;
+  if (a.rows == 0) {
+    p.full = 0;
+    p.split = 0;
+  }
+  if (err == cudaSuccess && p.full < tiles) {
+    const int n = tiles - p.full;
+    const long long need = static_cast<long long>(n) * (WT * WT / 4 / 256);
+    const long long cap = static_cast<long long>(device_sm_count()) * 8;
+    weight_grad_join_kernel<<<static_cast<unsigned>(need < cap ? need : cap), 256, 0, st>>>(
+        p, p.full, n);
+    err = cudaGetLastError();
+  }
+  const long long r0 = static_cast<long long>(plan.tiles_m) * WT;
+  const long long c0 = static_cast<long long>(plan.tiles_n) * WT;
+  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+  if (err == cudaSuccess && (r0 < pr || c0 < pc)) {
+    const dim3 grid(static_cast<unsigned>((pc + 1023) / 1024),
+                    static_cast<unsigned>(pr < 8192 ? pr : 8192));
+    weight_grad_pad_kernel<<<grid, 256, 0, st>>>(a, r0, c0);
+    err = cudaGetLastError();
+  }
   const double t = static_cast<double>(a.rows), o = static_cast<double>(a.outs),
                i = static_cast<double>(a.cols);
-  trace_end(rec, st, DASH_TRACE_GEMM_BF16, 2.0 * t * o * i,
+  trace_end(rec, st, DASH_TRACE_GEMM_BF16, 2.0 * t * o * i * plan.parts,
             t * o * dt_bytes(a.dt) + t * i * 33 / 32 + o * i * dt_bytes(a.odt));
-  return s;
+  return err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 }  // namespace dash

@@ -90,12 +90,14 @@ def test_weight_grad_refusals():
         assert wgrad(lib, **kw) == INVALID, kw
     assert wgrad(lib, wsb=0) == TOO_SMALL
     assert wgrad(lib, outs=0) == 0 and wgrad(lib, cols=0) == 0
+    assert wgrad(lib, dw=P + 2, B=128) == INVALID
+    assert wgrad(lib, outs=1 << 23, lddz=1 << 23, cols=1 << 23, ldw=1 << 23) == INVALID
     n = ctypes.c_size_t(0)
     size = lib.dash_weight_grad_workspace_size
-    assert size(4, 4, -1, 1, 0, ctypes.byref(n)) == INVALID
-    assert size(4, 4, 4, 7, 0, ctypes.byref(n)) == INVALID
-    assert size(4, 4, 4, 1, 100, ctypes.byref(n)) == INVALID
-    assert size(4, 4, 4, 1, 0, None) == INVALID
+    assert size(4, 4, -1, 1, 0, 0, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 7, 0, 0, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 1, 0, 100, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 1, 0, 0, None) == INVALID
 
 
 def test_format_names():
