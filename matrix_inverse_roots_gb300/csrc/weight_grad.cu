@@ -10,15 +10,23 @@
 //
 // Design (persistent, CTA pairs on 256 x 256 tiles of dW, cta_group::2; both operands lie
 // in memory with the token index outermost, so both are MN-major):
-//   warp 0       TMA producer of A: 128 columns of dz per CTA, 64 tokens per slot.
+//   warps 0, 3   TMA producers of A: 128 columns of dz per CTA, 64 tokens per slot, each
+//                loading 64 of the columns (one thread starts about 16 KB of tiled copies
+//                per 600 cycles, which the MMAs of a slot nearly take).
 //   warp 2       TMA producer of the codes: 128 columns, 64 tokens (8 KB) per slot.
-//   warps 4-11   converters: codes and scales (scales straight from global memory, two
-//                slots ahead) to bf16, into the 128-byte-swizzled layout the MMA reads.
-//   warp 3       hands a converted slot to the leader CTA: the converters' arrivals stay
-//                inside the CTA, and this one thread, which has no memory traffic of its
-//                own to wait for, makes the cluster-scope release.
+//   warps 4, 6, 7, 8, 10, 11  converters: codes and scales (scales straight from global
+//                memory, one slot ahead) to bf16, into the 128-byte-swizzled layout the MMA
+//                reads.  Pairs of warps take every third slot, so that the waits, loads and
+//                fences of three slots overlap.  None of them shares a scheduler with the
+//                MMA warp, whose few instructions would wait for theirs.
+//                A converter warp makes its writes visible to the tensor core (proxy
+//                fence) and arrives on the leader's barrier without a cluster-wide fence:
+//                what the arrival orders are writes to this CTA's own shared memory, which
+//                only this SM's tensor core reads, and they are complete before it.  (With
+//                a release at cluster scope each hand-over took about 1400 cycles, more
+//                than twice a slot's MMAs: 850 against 1400 TFLOP/s and more.)
 //   warp 1       of the leader issues the MMAs into one of two TMEM accumulators.
-//   warps 12-15  epilogue of the previous tile.
+//   warps 12-15  epilogue of the previous tile.  (Warps 5 and 9 idle.)
 // Tiles that do not fill a whole round of the pairs are split along the tokens; their
 // fp32 partial sums are joined, in order, by a second kernel.
 // Every wait is bounded (see mbar_wait); a time-out sets the device error flag, and the
@@ -47,9 +55,11 @@ constexpr int WB_BYTES = 128 * WK * 2;  // converted B slot: 128 columns, two bo
 constexpr int WQ_BYTES = 128 * WK;      // codes slot
 constexpr int W_BOX = WK * 128;         // one 64-column box of bf16: 64 rows of 128 B
 constexpr int NA = 5, NB = 5, NQ = 5;
-constexpr int W_CONV = 8, W_EPI = 4;    // converter and epilogue warps
-constexpr int W_THREADS = 32 * (4 + W_CONV + W_EPI);
-constexpr int W_BARS = 2 * NA + 2 * NQ + 3 * NB + 4 + 1;
+constexpr int W_GROUPS = 3;             // converter groups, each taking every 3rd slot
+constexpr int W_GW = 2;                 // warps of a group, each taking 32 of the 64 rows
+constexpr int W_EPI = 4, W_EPI0 = 12;   // epilogue warps
+constexpr int W_THREADS = 32 * (W_EPI0 + W_EPI);
+constexpr int W_BARS = 2 * NA + 2 * NQ + 2 * NB + 4 + 1;
 constexpr int W_SMEM = NA * WA_BYTES + NB * WB_BYTES + NQ * WQ_BYTES + 1024 + 512;
 static_assert(W_SMEM <= 232448, "shared memory budget");
 static_assert(8 * W_BARS + 16 <= 512, "barrier area");
@@ -172,32 +182,43 @@ __device__ __forceinline__ void finish_store(const WeightGradArgs& a, const floa
     if (i + j < pc) store_dt(a.dw, a.odt, at + j, v[j]);
 }
 
-// 16 codes (one 16-byte word of a row) to 16 bf16 numbers, two 16-byte words.
+__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The scale of a byte as a bf16 number, in both halves.
+__device__ __forceinline__ uint32_t scale_bf2(uint32_t byte) {
+  const uint32_t h = (byte << 7) | (byte == Q8_NAN_SCALE ? 0x40u : 0u);
+  return h | (h << 16);
+}
+
+// 16 codes (one 16-byte word of a row) times the scale s (bf16, in both halves), as 16
+// bf16 numbers in two 16-byte words.  Two at a time in packed bf16 arithmetic, of which
+// every result is exact.
 template <int FMT>
-__device__ __forceinline__ void convert16(const uint4& c, float s, uint4& lo, uint4& hi) {
+__device__ __forceinline__ void convert16(const uint4& c, uint32_t s, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t r[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float f[4];
+  for (int j = 0; j < 8; ++j) {
     if (FMT == DASH_Q8_INT8) {
-      // 2^23 + (q + 128) from the code's byte, less 2^23 + 128, times 2^e: all exact.
-      const uint32_t u = w[j] ^ 0x80808080u;
-      f[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.0f;
-      f[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.0f;
-      f[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - 8388736.0f;
-      f[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - 8388736.0f;
+      // q = (128 + low seven bits) - (128, or 256 for a negative q): 128 + x is 0x4300 + x
+      // in bf16 for x < 128, and 256 is 0x4380.
+      const uint32_t x = __byte_perm(w[j >> 1], 0u, (j & 1) ? 0x4342 : 0x4140);
+      r[j] = bf2_mul(bf2_sub((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u), s);
     } else {
-      // The code's exponent and mantissa as an fp32 number's, 2^120 too small.
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t b = w[j] >> (8 * k);
-        f[k] = __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7fu) << 20)) * 0x1p120f;
-      }
+      // The code's exponent and mantissa in the bf16 fields, 2^120 too small (0x7b80 is
+      // 2^120; subnormal codes are subnormal numbers).
+      const uint32_t x = __byte_perm(w[j >> 1], 0u, (j & 1) ? 0x3424 : 0x1404);
+      r[j] = bf2_mul(bf2_mul(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), 0x7b807b80u), s);
     }
-    // The products are bf16 numbers: their upper halves are all of them.
-    r[2 * j] = __byte_perm(__float_as_uint(f[0] * s), __float_as_uint(f[1] * s), 0x7632);
-    r[2 * j + 1] = __byte_perm(__float_as_uint(f[2] * s), __float_as_uint(f[3] * s), 0x7632);
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
@@ -220,11 +241,10 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   auto aempty = [&](int s) { return bar0 + 8u * (NA + s); };
   auto qfull = [&](int s) { return bar0 + 8u * (2 * NA + s); };
   auto qempty = [&](int s) { return bar0 + 8u * (2 * NA + NQ + s); };
-  auto bconv = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + s); };
-  auto bfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + NB + s); };
-  auto bempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 2 * NB + s); };
-  auto tfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 3 * NB + s); };
-  auto tempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 3 * NB + 2 + s); };
+  auto bfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + s); };
+  auto bempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + NB + s); };
+  auto tfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 2 * NB + s); };
+  auto tempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 2 * NB + 2 + s); };
   const uint32_t fin_bar = bar0 + 8u * (W_BARS - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8 * W_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * W_BARS + 8);
@@ -239,16 +259,15 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NA; ++s) {
-      mbar_init(afull(s), 1);
+      mbar_init(afull(s), 2);  // both producers of the leader
       mbar_init(aempty(s), 1);
     }
     for (int s = 0; s < NQ; ++s) {
       mbar_init(qfull(s), 1);
-      mbar_init(qempty(s), W_CONV);
+      mbar_init(qempty(s), W_GW);
     }
     for (int s = 0; s < NB; ++s) {
-      mbar_init(bconv(s), W_CONV);
-      mbar_init(bfull(s), 2);  // warp 3 of both CTAs
+      mbar_init(bfull(s), 2 * W_GW);  // the slot's converters of both CTAs
       mbar_init(bempty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -269,15 +288,16 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     if (lane == 0) {
-      // -------------------------------------------------------- A producer
+      // -------------------------------------------------------- A producers
+      const int half = warp == 0 ? 0 : 1;
       int s = 0;
       uint32_t ph = 0, armed = 0, armed_par = 0;
       bool ok = true;
       for (int u = cid; ok && u < p.units; u += ncl) {
         const Unit x = unit_at(u, p);
-        const int o0 = x.mt * WT + static_cast<int>(crank) * 128;
+        const int o0 = x.mt * WT + static_cast<int>(crank) * 128 + half * 64;
         for (int kb = x.k0; ok && kb < x.k1; ++kb) {
           for (int part = 0; part < p.parts; ++part) {
             if (!mbar_wait(aempty(s), ph ^ 1u, abort_flag)) {
@@ -286,15 +306,13 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             }
             uint32_t fb = afull(s);
             if (leader) {
-              mbar_arrive_expect_tx(fb, 2 * WA_BYTES);
+              mbar_arrive_expect_tx(fb, 2 * W_BOX);
               armed |= 1u << s;
               armed_par = (armed_par & ~(1u << s)) | (ph << s);
             } else {
               fb = mapa_shared(fb, 0);
             }
-            const uint32_t dst = sbase + s * WA_BYTES;
-            tma_load_3d_pair(dst, &tA, fb, o0, kb * WK, part);
-            tma_load_3d_pair(dst + W_BOX, &tA, fb, o0 + 64, kb * WK, part);
+            tma_load_3d_pair(sbase + s * WA_BYTES + half * W_BOX, &tA, fb, o0, kb * WK, part);
             if (++s == NA) {
               s = 0;
               ph ^= 1u;
@@ -334,27 +352,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         for (int i = 0; i < NQ; ++i)
           if (armed & (1u << i)) mbar_wait_drain(qfull(i), (armed_par >> i) & 1u);
     }
-  } else if (warp == 3) {
-    if (lane == 0) {
-      // -------------------------------------------------------- hand-over of B slots
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int u = cid; ok && u < p.units; u += ncl) {
-        const Unit x = unit_at(u, p);
-        for (int kb = x.k0; kb < x.k1; ++kb) {
-          if (!mbar_wait(bconv(s), ph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_cluster(mapa_shared(bfull(s), 0));
-          if (++s == NB) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-      }
-    }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // -------------------------------------------------------- MMA issuer
@@ -368,7 +365,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * WT);
         for (int kb = x.k0; ok && kb < x.k1; ++kb) {
-          if (!mbar_wait_cluster(bfull(sb), pb, abort_flag)) {
+          if (!mbar_wait(bfull(sb), pb, abort_flag)) {
             ok = false;
             break;
           }
@@ -407,68 +404,81 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       mma_commit_pair(fin_bar);
       mbar_wait_drain(fin_bar, 0);
     }
-  } else if (warp < 4 + W_CONV) {
+  } else if (warp < W_EPI0) {
     // ---------------------------------------------------------- converters
-    // Thread c of 256: row t = c / 8 (and t + 32) of the slot, 16 columns from 16 (c % 8).
-    const int c = threadIdx.x - 128;
-    const int t = c >> 3, c16 = c & 7;
-    int sq = 0, sb = 0;
-    uint32_t pq = 0, pb = 0;
-    bool ok = true;
+    // Converter number 0 .. 5 of the warp (5 and 9 have none).  Group `grp` takes the slots
+    // whose running number is grp modulo W_GROUPS; a warp takes 32 of a slot's rows, eight
+    // lanes a row of 128 columns, four rows at a time.
+    const int conv = (warp & 3) == 1 ? -1 : (warp - 4) / 4 * 3 + ((warp & 3) == 0 ? 0 : (warp & 3) - 1);
+    const int grp = conv / W_GW;
+    const int t0 = (conv % W_GW) * 32 + (lane >> 3), c16 = lane & 7;
+    // 16-byte words w and w + 1 of a row at the swizzled places; the upper box's lanes
+    // write the odd word first, so that a row's eight lanes hit all banks once.
+    const int w = (c16 & 3) * 2, odd = c16 >> 2;
+    const int qoff = t0 * 128 + c16 * 16;
+    const int boff = odd * W_BOX + t0 * 128;
+    int n = 0;  // running number of the unit's first slot, modulo NMOD
+    constexpr int NMOD = W_GROUPS * NQ * NB * 2;
+    const bool words = (p.ng & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3u) == 0;
+    bool ok = conv >= 0;
     for (int u = cid; ok && u < p.units; u += ncl) {
       const Unit x = unit_at(u, p);
-      const long long g = x.nt * (WT / Q8_GROUP) + static_cast<int>(crank) * 4 + (c16 >> 1);
-      const bool gin = g < p.ng;
-      // Scale bytes of this thread's two rows of slot kb; 0 (a scale of 0) outside.
+      const int g0 = x.nt * (WT / Q8_GROUP) + static_cast<int>(crank) * 4;
+      // The four scale bytes of row 32 (conv % W_GW) + lane of slot kb; 0 (a scale of 0)
+      // outside.
       auto scales = [&](int kb) -> uint32_t {
+        const long long r = static_cast<long long>(kb) * WK + (conv % W_GW) * 32 + lane;
         uint32_t v = 0;
-        const long long r = static_cast<long long>(kb) * WK + t;
-        if (gin && kb < x.k1) {
-          if (r < p.rows) v = p.scale[r * p.ng + g];
-          if (r + 32 < p.rows) v |= static_cast<uint32_t>(p.scale[(r + 32) * p.ng + g]) << 8;
+        if (kb < x.k1 && r < p.rows && g0 < p.ng) {
+          const uint8_t* sp = p.scale + r * p.ng + g0;
+          if (words) {
+            v = *reinterpret_cast<const uint32_t*>(sp);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (g0 + j < p.ng) v |= static_cast<uint32_t>(sp[j]) << (8 * j);
+          }
         }
         return v;
       };
-      uint32_t v0 = scales(x.k0), v1 = scales(x.k0 + 1);
-      for (int kb = x.k0; kb < x.k1; ++kb) {
-        const uint32_t v2 = scales(kb + 2);
-        if (!mbar_wait(qfull(sq), pq, abort_flag) || !mbar_wait(bempty(sb), pb ^ 1u, abort_flag)) {
+      int kb = x.k0 + (grp - n % W_GROUPS + W_GROUPS) % W_GROUPS;
+      uint32_t sc = scales(kb);
+      for (; kb < x.k1; kb += W_GROUPS) {
+        const int m = n + (kb - x.k0);  // running number of this slot
+        const int sq = m % NQ, sb = m % NB;
+        const uint32_t next = scales(kb + W_GROUPS);
+        // The B slot first, then the codes are given back: a later slot's codes can then
+        // only be there once this wait is over, so that no group waits on a barrier two
+        // phases ahead of it (a parity could not tell them apart).
+        static_assert(NQ <= NB, "codes of slot m imply that slot m - NB passed its wait");
+        if (!mbar_wait(qfull(sq), (m / NQ) & 1u, abort_flag) ||
+            !mbar_wait(bempty(sb), ((m / NB) & 1u) ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
-        const uint8_t* src = smem + OFF_Q + sq * WQ_BYTES + c16 * 16;
-        const uint4 q0 = *reinterpret_cast<const uint4*>(src + t * 128);
-        const uint4 q1 = *reinterpret_cast<const uint4*>(src + (t + 32) * 128);
+        uint4 q[8];
+        const uint8_t* src = smem + OFF_Q + sq * WQ_BYTES + qoff;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = *reinterpret_cast<const uint4*>(src + j * 4 * 128);
         __syncwarp();
         if (lane == 0) mbar_arrive(qempty(sq));
-        uint8_t* box = smem + OFF_B + sb * WB_BYTES + (c16 >> 2) * W_BOX;
-        // 16-byte words 2 (c16 % 4) and + 1 of the row, at the swizzled places; the upper
-        // box's threads write the odd word first, so that a row's eight threads hit all
-        // banks once.
-        const int w = (c16 & 3) * 2, odd = c16 >> 2, sw = t & 7;
-        uint8_t* r0 = box + t * 128;
-        uint4 lo, hi;
-        convert16<FMT>(q0, q8_scale(v0 & 0xffu), lo, hi);
-        *reinterpret_cast<uint4*>(r0 + (((w + odd) ^ sw) << 4)) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(r0 + (((w + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
-        r0 += 32 * 128;  // (t + 32) % 8 == t % 8
-        convert16<FMT>(q1, q8_scale(v0 >> 8), lo, hi);
-        *reinterpret_cast<uint4*>(r0 + (((w + odd) ^ sw) << 4)) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(r0 + (((w + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+        uint8_t* dst = smem + OFF_B + sb * WB_BYTES + boff;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t four = __shfl_sync(0xffffffffu, sc, j * 4 + (lane >> 3));
+          uint4 lo, hi;
+          convert16<FMT>(q[j], scale_bf2((four >> ((c16 >> 1) * 8)) & 0xffu), lo, hi);
+          const int sw = (t0 + j * 4) & 7;
+          uint8_t* r0 = dst + j * 4 * 128;
+          *reinterpret_cast<uint4*>(r0 + (((w + odd) ^ sw) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(r0 + (((w + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+        }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bconv(sb));
-        v0 = v1;
-        v1 = v2;
-        if (++sq == NQ) {
-          sq = 0;
-          pq ^= 1u;
-        }
-        if (++sb == NB) {
-          sb = 0;
-          pb ^= 1u;
-        }
+        if (lane == 0) mbar_arrive_remote(mapa_shared(bfull(sb), 0));
+        sc = next;
       }
+      n = (n + x.k1 - x.k0) % NMOD;
     }
   } else {
     // ---------------------------------------------------------- epilogue
