@@ -14,19 +14,22 @@
 //                loading 64 of the columns (one thread starts about 16 KB of tiled copies
 //                per 600 cycles, which the MMAs of a slot nearly take).
 //   warp 2       TMA producer of the codes: 128 columns, 64 tokens (8 KB) per slot.
-//   warps 4, 6, 7, 8, 10, 11  converters: codes and scales (scales straight from global
+//   warps 4, 6-8, 10-15  converters: codes and scales (scales straight from global
 //                memory, one slot ahead) to bf16, into the 128-byte-swizzled layout the MMA
-//                reads.  Pairs of warps take every third slot, so that the waits, loads and
-//                fences of three slots overlap.  None of them shares a scheduler with the
-//                MMA warp, whose few instructions would wait for theirs.
+//                reads.  A slot takes a warp pair about 1500 cycles from its codes to its
+//                hand-over, three times its MMAs, so every ring slot has a pair of its
+//                own.  Measured at 16384 x 8192 x 8192 with int8 codes and five slots:
+//                three pairs 1340 TFLOP/s, four 1570, five 1600.  All but one of them
+//                stay off the scheduler of the MMA warp, whose few instructions would
+//                wait for theirs (hence the idle warps 5 and 9).
 //                A converter warp makes its writes visible to the tensor core (proxy
 //                fence) and arrives on the leader's barrier without a cluster-wide fence:
 //                what the arrival orders are writes to this CTA's own shared memory, which
 //                only this SM's tensor core reads, and they are complete before it.  (With
 //                a release at cluster scope each hand-over took about 1400 cycles, more
-//                than twice a slot's MMAs: 850 against 1400 TFLOP/s and more.)
+//                than twice a slot's MMAs, and the product ran at 850 TFLOP/s.)
 //   warp 1       of the leader issues the MMAs into one of two TMEM accumulators.
-//   warps 12-15  epilogue of the previous tile.  (Warps 5 and 9 idle.)
+//   warps 16-19  epilogue of the previous tile.
 // Tiles that do not fill a whole round of the pairs are split along the tokens; their
 // fp32 partial sums are joined, in order, by a second kernel.
 // Every wait is bounded (see mbar_wait); a time-out sets the device error flag, and the
@@ -50,23 +53,27 @@ namespace {
 
 constexpr int WT = 256;              // tile of dW per CTA pair (both directions)
 constexpr int WK = 64;               // tokens per slot
-constexpr int WA_BYTES = 128 * WK * 2;  // A slot: 128 columns of dz, two 64-column boxes
-constexpr int WB_BYTES = 128 * WK * 2;  // converted B slot: 128 columns, two boxes
-constexpr int WQ_BYTES = 128 * WK;      // codes slot
-constexpr int W_BOX = WK * 128;         // one 64-column box of bf16: 64 rows of 128 B
-constexpr int NA = 5, NB = 5, NQ = 5;
-constexpr int W_GROUPS = 3;             // converter groups, each taking every 3rd slot
-constexpr int W_GW = 2;                 // warps of a group, each taking 32 of the 64 rows
-constexpr int W_EPI = 4, W_EPI0 = 12;   // epilogue warps
+constexpr int W_BOX = WK * 128;      // one box: 64 tokens of 64 bf16 columns or 128 codes
+constexpr int W_GW = 2;              // warps of a converter group, each taking 32 of 64 rows
+constexpr int W_EPI = 4, W_EPI0 = 16;  // epilogue warps
 constexpr int W_THREADS = 32 * (W_EPI0 + W_EPI);
-constexpr int W_BARS = 2 * NA + 2 * NQ + 2 * NB + 4 + 1;
-constexpr int W_SMEM = NA * WA_BYTES + NB * WB_BYTES + NQ * WQ_BYTES + 1024 + 512;
-static_assert(W_SMEM <= 232448, "shared memory budget");
-static_assert(8 * W_BARS + 16 <= 512, "barrier area");
+
+// A ring slot holds 64 tokens: PARTS tiles of A (128 columns of dz in two boxes), the
+// converted B (128 columns in two boxes) and the codes (one box).
+template <int PARTS>
+struct WCfg {
+  static constexpr int OFF_B = PARTS * 2 * W_BOX;
+  static constexpr int OFF_Q = OFF_B + 2 * W_BOX;
+  static constexpr int SLOT = OFF_Q + W_BOX;
+  static constexpr int NS = (232448 - 1536) / SLOT;  // 5, 4, 3 slots
+  static constexpr int CONV = NS * W_GW;             // converter warps
+  static constexpr int BARS = 4 * NS + 4 + 1;
+  static constexpr int SMEM = NS * SLOT + 1024 + 512;
+  static_assert(NS >= 3 && CONV <= 10 && 8 * BARS + 16 <= 512, "ring, warps, barrier area");
+};
 
 struct WParams {
   int nkb;             // slots of 64 tokens
-  int parts;           // bf16 parts of dz
   int tiles_m, tiles_n;
   int full;            // tiles computed whole
   int split, kper;     // the others: `split` units of kper slots each
@@ -88,6 +95,19 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& mt
   const int r = t - g * per;
   mt = g * G + r % h;
   nt = r / h;
+}
+
+// Whether the phase of the given parity is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 struct Unit {
@@ -193,61 +213,70 @@ __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The scale of a byte as a bf16 number, in both halves.
-__device__ __forceinline__ uint32_t scale_bf2(uint32_t byte) {
-  const uint32_t h = (byte << 7) | (byte == Q8_NAN_SCALE ? 0x40u : 0u);
-  return h | (h << 16);
+// 2^e as a bf16 number in both halves, from a word with the scale byte in its bytes 0 and
+// 2; NaN (not the infinity that the shift alone would make) for the byte 255.
+__device__ __forceinline__ uint32_t scale_bf2(uint32_t x) {
+  return (x << 7) | (((x + 0x00010001u) >> 2) & 0x00400040u);
 }
 
 // 16 codes (one 16-byte word of a row) times the scale s (bf16, in both halves), as 16
 // bf16 numbers in two 16-byte words.  Two at a time in packed bf16 arithmetic, of which
-// every result is exact.
+// every result is exact.  Every four come out in the order 0, 2, 1, 3, which a code word's
+// two halves give without a permutation; the epilogue puts the columns back (tmem_col).
 template <int FMT>
 __device__ __forceinline__ void convert16(const uint4& c, uint32_t s, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (FMT == DASH_Q8_INT8) {
-      // q = (128 + low seven bits) - (128, or 256 for a negative q): 128 + x is 0x4300 + x
-      // in bf16 for x < 128, and 256 is 0x4380.
-      const uint32_t x = __byte_perm(w[j >> 1], 0u, (j & 1) ? 0x4342 : 0x4140);
-      r[j] = bf2_mul(bf2_sub((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u), s);
-    } else {
-      // The code's exponent and mantissa in the bf16 fields, 2^120 too small (0x7b80 is
-      // 2^120; subnormal codes are subnormal numbers).
-      const uint32_t x = __byte_perm(w[j >> 1], 0u, (j & 1) ? 0x3424 : 0x1404);
-      r[j] = bf2_mul(bf2_mul(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), 0x7b807b80u), s);
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (FMT == DASH_Q8_INT8) {
+        // q = (128 + low seven bits) - (128, or 256 for a negative q): 128 + x is
+        // 0x4300 + x in bf16 for x < 128, and 256 is 0x4380.
+        const uint32_t x = h ? w[j] >> 8 : w[j];
+        r[2 * j + h] = bf2_mul(
+            bf2_sub((x & 0x007f007fu) | 0x43004300u, (x & 0x00800080u) | 0x43004300u), s);
+      } else {
+        // The code's exponent and mantissa in the bf16 fields, 2^120 too small (0x7b80 is
+        // 2^120; subnormal codes are subnormal numbers).
+        const uint32_t m = h ? w[j] >> 4 : w[j] << 4, g = h ? w[j] : w[j] << 8;
+        r[2 * j + h] =
+            bf2_mul(bf2_mul((m & 0x07f007f0u) | (g & 0x80008000u), 0x7b807b80u), s);
+      }
     }
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-template <int FMT>
+// Accumulator column of a tile's column, within 16.
+__host__ __device__ constexpr int tmem_col(int j) {
+  return (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1);
+}
+
+template <int FMT, int PARTS>
 __global__ void __launch_bounds__(W_THREADS, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tQ,
                        const __grid_constant__ WParams p) {
+  using C = WCfg<PARTS>;
+  constexpr int NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw_base + pad;
-  constexpr int OFF_B = NA * WA_BYTES;
-  constexpr int OFF_Q = OFF_B + NB * WB_BYTES;
-  constexpr int OFF_BAR = OFF_Q + NQ * WQ_BYTES;
-  const uint32_t bar0 = sbase + OFF_BAR;
-  auto afull = [&](int s) { return bar0 + 8u * s; };
-  auto aempty = [&](int s) { return bar0 + 8u * (NA + s); };
-  auto qfull = [&](int s) { return bar0 + 8u * (2 * NA + s); };
-  auto qempty = [&](int s) { return bar0 + 8u * (2 * NA + NQ + s); };
-  auto bfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + s); };
-  auto bempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + NB + s); };
-  auto tfull = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 2 * NB + s); };
-  auto tempty = [&](int s) { return bar0 + 8u * (2 * NA + 2 * NQ + 2 * NB + 2 + s); };
-  const uint32_t fin_bar = bar0 + 8u * (W_BARS - 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8 * W_BARS);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + 8 * W_BARS + 8);
+  const uint32_t bar0 = sbase + NS * C::SLOT;
+  auto full = [&](int s) { return bar0 + 8u * s; };             // A landed, B converted
+  auto empty = [&](int s) { return bar0 + 8u * (NS + s); };     // the MMAs have read both
+  auto qfull = [&](int s) { return bar0 + 8u * (2 * NS + s); };
+  auto qempty = [&](int s) { return bar0 + 8u * (3 * NS + s); };
+  auto tfull = [&](int s) { return bar0 + 8u * (4 * NS + s); };
+  auto tempty = [&](int s) { return bar0 + 8u * (4 * NS + 2 + s); };
+  const uint32_t fin_bar = bar0 + 8u * (C::BARS - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + NS * C::SLOT + 8 * C::BARS);
+  volatile int* abort_flag =
+      reinterpret_cast<volatile int*>(smem + NS * C::SLOT + 8 * C::BARS + 8);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -258,17 +287,13 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   constexpr uint16_t kMask = 3;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NA; ++s) {
-      mbar_init(afull(s), 2);  // both producers of the leader
-      mbar_init(aempty(s), 1);
-    }
-    for (int s = 0; s < NQ; ++s) {
+    for (int s = 0; s < NS; ++s) {
+      // Of the leader: its two producers (the bytes of both CTAs) and the slot's
+      // converters of both CTAs.
+      mbar_init(full(s), 2 + 2 * W_GW);
+      mbar_init(empty(s), 1);
       mbar_init(qfull(s), 1);
       mbar_init(qempty(s), W_GW);
-    }
-    for (int s = 0; s < NB; ++s) {
-      mbar_init(bfull(s), 2 * W_GW);  // the slot's converters of both CTAs
-      mbar_init(bempty(s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(tfull(s), 1);
@@ -298,31 +323,35 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       for (int u = cid; ok && u < p.units; u += ncl) {
         const Unit x = unit_at(u, p);
         const int o0 = x.mt * WT + static_cast<int>(crank) * 128 + half * 64;
-        for (int kb = x.k0; ok && kb < x.k1; ++kb) {
-          for (int part = 0; part < p.parts; ++part) {
-            if (!mbar_wait(aempty(s), ph ^ 1u, abort_flag)) {
-              ok = false;
-              break;
-            }
-            uint32_t fb = afull(s);
-            if (leader) {
-              mbar_arrive_expect_tx(fb, 2 * W_BOX);
-              armed |= 1u << s;
-              armed_par = (armed_par & ~(1u << s)) | (ph << s);
-            } else {
-              fb = mapa_shared(fb, 0);
-            }
-            tma_load_3d_pair(sbase + s * WA_BYTES + half * W_BOX, &tA, fb, o0, kb * WK, part);
-            if (++s == NA) {
-              s = 0;
-              ph ^= 1u;
-            }
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          if (!mbar_wait(empty(s), ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint32_t fb = full(s);
+          if (leader) {
+            mbar_arrive_expect_tx(fb, 2 * PARTS * W_BOX);
+            armed |= 1u << s;
+            armed_par = (armed_par & ~(1u << s)) | (ph << s);
+          } else {
+            fb = mapa_shared(fb, 0);
+          }
+          const uint32_t dst = sbase + s * C::SLOT + half * W_BOX;
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+            tma_load_3d_pair(dst + part * 2 * W_BOX, &tA, fb, o0, kb * WK, part);
+          if (++s == NS) {
+            s = 0;
+            ph ^= 1u;
           }
         }
       }
+      // After a time-out, one that arms it for both CTAs waits for the copies it counts.
+      // Its barrier also counts the converters, which may have stopped: the wait is
+      // bounded all the same.
       if (!ok)
-        for (int i = 0; i < NA; ++i)
-          if (armed & (1u << i)) mbar_wait_drain(afull(i), (armed_par >> i) & 1u);
+        for (int i = 0; i < NS; ++i)
+          if (armed & (1u << i)) mbar_wait_drain(full(i), (armed_par >> i) & 1u);
     }
   } else if (warp == 2) {
     if (lane == 0) {
@@ -338,62 +367,59 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(qfull(s), WQ_BYTES);
+          mbar_arrive_expect_tx(qfull(s), W_BOX);
           armed |= 1u << s;
           armed_par = (armed_par & ~(1u << s)) | (ph << s);
-          tma_load_3d(sbase + OFF_Q + s * WQ_BYTES, &tQ, qfull(s), i0, kb * WK, 0);
-          if (++s == NQ) {
+          tma_load_3d(sbase + s * C::SLOT + C::OFF_Q, &tQ, qfull(s), i0, kb * WK, 0);
+          if (++s == NS) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
       if (!ok)
-        for (int i = 0; i < NQ; ++i)
+        for (int i = 0; i < NS; ++i)
           if (armed & (1u << i)) mbar_wait_drain(qfull(i), (armed_par >> i) & 1u);
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // -------------------------------------------------------- MMA issuer
+      // The tensor cores take about 520 cycles for a slot's MMAs of one part; this
+      // thread has to come round in less.  So: one barrier to wait for and one to signal
+      // per slot, the next slot's barrier looked at before this slot's MMAs are issued,
+      // and descriptors that are one addition away from a constant.
       const uint32_t idesc = make_idesc(1, 1, 1, 256, 256);
-      int sa = 0, sb = 0, acc = 0;
-      uint32_t pa = 0, pb = 0, pacc = 0;
-      bool ok = true;
+      const uint64_t d0 = smem_desc(sbase, W_BOX, 1024, LAYOUT_SW128);
+      int s = 0, acc = 0;
+      uint32_t ph = 0, pacc = 0;
+      bool ok = true, ready = false;
       for (int u = cid; ok && u < p.units; u += ncl) {
         const Unit x = unit_at(u, p);
         if (!mbar_wait(tempty(acc), pacc ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * WT);
-        for (int kb = x.k0; ok && kb < x.k1; ++kb) {
-          if (!mbar_wait(bfull(sb), pb, abort_flag)) {
+        uint32_t accumulate = 0;
+        for (int kb = x.k0; kb < x.k1; ++kb) {
+          if (!ready && !mbar_wait(full(s), ph, abort_flag)) {
             ok = false;
             break;
           }
-          const uint32_t sB = sbase + OFF_B + sb * WB_BYTES;
-          for (int part = 0; part < p.parts; ++part) {
-            if (!mbar_wait(afull(sa), pa, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sA = sbase + sa * WA_BYTES;
+          const int sn = s + 1 == NS ? 0 : s + 1;
+          const uint32_t pn = sn == 0 ? ph ^ 1u : ph;
+          ready = mbar_test(full(sn), pn);
+          tc_fence_after();
+          const uint64_t da = d0 + static_cast<uint32_t>(s * (C::SLOT >> 4));
 #pragma unroll
-            for (int kk = 0; kk < WK / 16; ++kk)
-              mma_f16_pair(d, smem_desc(sA + kk * 16 * 128, W_BOX, 1024, LAYOUT_SW128),
-                           smem_desc(sB + kk * 16 * 128, W_BOX, 1024, LAYOUT_SW128), idesc,
-                           (kb > x.k0 || part > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair_mc(aempty(sa), kMask);
-            if (++sa == NA) {
-              sa = 0;
-              pa ^= 1u;
+          for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int kk = 0; kk < WK / 16; ++kk) {
+              mma_f16_pair(d, da + ((part * 2 * W_BOX + kk * 16 * 128) >> 4),
+                           da + ((C::OFF_B + kk * 16 * 128) >> 4), idesc, accumulate);
+              accumulate = 1;
             }
-          }
-          if (!ok) break;
-          mma_commit_pair_mc(bempty(sb), kMask);
-          if (++sb == NB) {
-            sb = 0;
-            pb ^= 1u;
-          }
+          mma_commit_pair_mc(empty(s), kMask);
+          s = sn;
+          ph = pn;
         }
         if (!ok) break;
         mma_commit_pair_mc(tfull(acc), kMask);
@@ -406,21 +432,26 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     }
   } else if (warp < W_EPI0) {
     // ---------------------------------------------------------- converters
-    // Converter number 0 .. 5 of the warp (5 and 9 have none).  Group `grp` takes the slots
-    // whose running number is grp modulo W_GROUPS; a warp takes 32 of a slot's rows, eight
-    // lanes a row of 128 columns, four rows at a time.
-    const int conv = (warp & 3) == 1 ? -1 : (warp - 4) / 4 * 3 + ((warp & 3) == 0 ? 0 : (warp & 3) - 1);
-    const int grp = conv / W_GW;
-    const int t0 = (conv % W_GW) * 32 + (lane >> 3), c16 = lane & 7;
-    // 16-byte words w and w + 1 of a row at the swizzled places; the upper box's lanes
-    // write the odd word first, so that a row's eight lanes hit all banks once.
-    const int w = (c16 & 3) * 2, odd = c16 >> 2;
-    const int qoff = t0 * 128 + c16 * 16;
-    const int boff = odd * W_BOX + t0 * 128;
-    int n = 0;  // running number of the unit's first slot, modulo NMOD
-    constexpr int NMOD = W_GROUPS * NQ * NB * 2;
+    // Converter number 0 .. 9 of the warp (5 and 9 have none).  Group s takes ring slot s,
+    // every time: what it waits on there it has followed phase by phase, so a parity is
+    // never ambiguous.  A warp takes 32 of a slot's rows, eight lanes a row of 128 columns,
+    // four rows at a time.
+    const int conv = (warp == 5 || warp == 9) ? -1 : warp - 4 - (warp > 5) - (warp > 9);
+    const int s = conv / W_GW;
+    uint32_t par = 0;
+    // The lanes of the upper 64 columns (box 1) take the neighbouring row, whose swizzle
+    // differs in the lowest bit: the eight lanes of an access then hit all banks once.
+    const int c16 = lane & 7, odd = c16 >> 2;
+    const int rl = (lane >> 3) ^ odd;  // row, of the four
+    const int t0 = (conv % W_GW) * 32 + rl;
+    const int w = (c16 & 3) * 2;       // its 16-byte words are w and w + 1 of the box's row
+    const int qoff = C::OFF_Q + t0 * 128 + c16 * 16;
+    const int boff = C::OFF_B + odd * W_BOX + t0 * 128;
+    uint8_t* const slot = smem + s * C::SLOT;
+    const uint32_t sel = 0x4040u | ((c16 >> 1) * 0x0101u);  // the group's byte to bytes 0, 2
+    int ahead = s;  // slots from the unit's first to the group's next
     const bool words = (p.ng & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3u) == 0;
-    bool ok = conv >= 0;
+    bool ok = conv >= 0 && conv < C::CONV;
     for (int u = cid; ok && u < p.units; u += ncl) {
       const Unit x = unit_at(u, p);
       const int g0 = x.nt * (WT / Q8_GROUP) + static_cast<int>(crank) * 4;
@@ -441,44 +472,38 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         }
         return v;
       };
-      int kb = x.k0 + (grp - n % W_GROUPS + W_GROUPS) % W_GROUPS;
+      int kb = x.k0 + ahead;
       uint32_t sc = scales(kb);
-      for (; kb < x.k1; kb += W_GROUPS) {
-        const int m = n + (kb - x.k0);  // running number of this slot
-        const int sq = m % NQ, sb = m % NB;
-        const uint32_t next = scales(kb + W_GROUPS);
-        // The B slot first, then the codes are given back: a later slot's codes can then
-        // only be there once this wait is over, so that no group waits on a barrier two
-        // phases ahead of it (a parity could not tell them apart).
-        static_assert(NQ <= NB, "codes of slot m imply that slot m - NB passed its wait");
-        if (!mbar_wait(qfull(sq), (m / NQ) & 1u, abort_flag) ||
-            !mbar_wait(bempty(sb), ((m / NB) & 1u) ^ 1u, abort_flag)) {
+      for (; kb < x.k1; kb += NS) {
+        const uint32_t next = scales(kb + NS);
+        if (!mbar_wait(qfull(s), par, abort_flag) || !mbar_wait(empty(s), par ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
         uint4 q[8];
-        const uint8_t* src = smem + OFF_Q + sq * WQ_BYTES + qoff;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = *reinterpret_cast<const uint4*>(src + j * 4 * 128);
+        for (int j = 0; j < 8; ++j)
+          q[j] = *reinterpret_cast<const uint4*>(slot + qoff + j * 4 * 128);
         __syncwarp();
-        if (lane == 0) mbar_arrive(qempty(sq));
-        uint8_t* dst = smem + OFF_B + sb * WB_BYTES + boff;
+        if (lane == 0) mbar_arrive(qempty(s));
+        uint8_t* dst = slot + boff;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t four = __shfl_sync(0xffffffffu, sc, j * 4 + (lane >> 3));
+          const uint32_t four = __shfl_sync(0xffffffffu, sc, j * 4 + rl);
           uint4 lo, hi;
-          convert16<FMT>(q[j], scale_bf2((four >> ((c16 >> 1) * 8)) & 0xffu), lo, hi);
+          convert16<FMT>(q[j], scale_bf2(__byte_perm(four, 0u, sel)), lo, hi);
           const int sw = (t0 + j * 4) & 7;
           uint8_t* r0 = dst + j * 4 * 128;
-          *reinterpret_cast<uint4*>(r0 + (((w + odd) ^ sw) << 4)) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(r0 + (((w + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+          *reinterpret_cast<uint4*>(r0 + ((w ^ sw) << 4)) = lo;
+          *reinterpret_cast<uint4*>(r0 + (((w + 1) ^ sw) << 4)) = hi;
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(bfull(sb), 0));
+        if (lane == 0) mbar_arrive_remote(mapa_shared(full(s), 0));
         sc = next;
+        par ^= 1u;
       }
-      n = (n + x.k1 - x.k0) % NMOD;
+      ahead = kb - x.k1;
     }
   } else {
     // ---------------------------------------------------------- epilogue
@@ -504,7 +529,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         }
         float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[tmem_col(j)]);
         if (x.part >= 0) {
           float4* d = reinterpret_cast<float4*>(
               p.partial + (static_cast<long long>(x.part) * WT + row) * WT + cc * 16);
@@ -640,6 +665,21 @@ bool make_map(CUtensorMap* m, const void* base, bool bytes, uint64_t inner, uint
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+typedef void (*WKernel)(CUtensorMap, CUtensorMap, WParams);
+
+WKernel kernel_of(int fmt, int parts) {
+  if (fmt == DASH_Q8_INT8)
+    return parts == 1   ? weight_grad_kernel<DASH_Q8_INT8, 1>
+           : parts == 2 ? weight_grad_kernel<DASH_Q8_INT8, 2>
+                        : weight_grad_kernel<DASH_Q8_INT8, 3>;
+  return parts == 1   ? weight_grad_kernel<DASH_Q8_E4M3, 1>
+         : parts == 2 ? weight_grad_kernel<DASH_Q8_E4M3, 2>
+                      : weight_grad_kernel<DASH_Q8_E4M3, 3>;
+}
+int smem_of(int parts) {
+  return parts == 1 ? WCfg<1>::SMEM : (parts == 2 ? WCfg<2>::SMEM : WCfg<3>::SMEM);
+}
+
 // CTA pairs that can be resident at once, per device; 0 on error.
 int resident_pairs() {
   static int cache[64] = {0};
@@ -654,16 +694,20 @@ int resident_pairs() {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(512, 1, 1);
     cfg.blockDim = dim3(W_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = W_SMEM;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    for (auto k : {weight_grad_kernel<DASH_Q8_INT8>, weight_grad_kernel<DASH_Q8_E4M3>})
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W_SMEM) !=
-          cudaSuccess)
-        return 0;
-    if (cudaOccupancyMaxActiveClusters(&n, weight_grad_kernel<DASH_Q8_INT8>, &cfg) != cudaSuccess)
-      return 0;
+    int n = 1 << 30;
+    for (int fmt : {DASH_Q8_INT8, DASH_Q8_E4M3})
+      for (int parts = 1; parts <= 3; ++parts) {
+        const void* k = reinterpret_cast<const void*>(kernel_of(fmt, parts));
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(parts)) !=
+            cudaSuccess)
+          return 0;
+        cfg.dynamicSmemBytes = smem_of(parts);
+        int m = 0;
+        if (cudaOccupancyMaxActiveClusters(&m, k, &cfg) != cudaSuccess) return 0;
+        n = m < n ? m : n;
+      }
     const int sms = device_sm_count() / 2;
     cache[dev] = n < sms ? n : sms;
   }
@@ -771,7 +815,6 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
   cudaError_t err = cudaSuccess;
   WParams p = {};
   p.nkb = plan.nkb;
-  p.parts = plan.parts;
   p.tiles_m = plan.tiles_m;
   p.tiles_n = plan.tiles_n;
   p.full = plan.full;
@@ -816,13 +859,11 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (plan.units < pairs ? plan.units : pairs)), 1, 1);
     cfg.blockDim = dim3(W_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = W_SMEM;
+    cfg.dynamicSmemBytes = smem_of(plan.parts);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto k = a.fmt == DASH_Q8_INT8 ? weight_grad_kernel<DASH_Q8_INT8>
-                                   : weight_grad_kernel<DASH_Q8_E4M3>;
-    err = cudaLaunchKernelEx(&cfg, k, tA, tQ, p);
+    err = cudaLaunchKernelEx(&cfg, kernel_of(a.fmt, plan.parts), tA, tQ, p);
   }
   const int tiles = plan.tiles_m * plan.tiles_n;
   if (a.rows == 0) {
