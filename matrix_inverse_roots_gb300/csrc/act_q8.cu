@@ -1,4 +1,9 @@
 // 8-bit activation checkpoints: a matrix to codes and scales, and back.
+//
+// Both are one pass over the data, bound by HBM.  A thread holds Q8_U vectors of eight
+// columns (four neighbouring lanes share a group, so its largest magnitude takes two
+// shuffles) and issues all their loads before the first use.  Q8_U is 4, about 16 to 32
+// KB of reads in flight per 256 threads.
 #include "act_q8.cuh"
 #include "dash_internal.h"
 #include "train_internal.h"
@@ -6,100 +11,164 @@
 namespace dash {
 
 constexpr int Q8_THREADS = 256;
+constexpr int Q8_U = 4;
 
-// One warp per group of 32 columns, a lane per column.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(Q8_THREADS)
-    act_compress_kernel(const T* x, long long rows, long long cols, long long ld, long long ng,
-                        uint8_t* q, uint8_t* scale) {
-  const int lane = threadIdx.x & 31;
-  const long long total = rows * ng;
-  const long long step = static_cast<long long>(gridDim.x) * (Q8_THREADS / 32);
-  for (long long i = static_cast<long long>(blockIdx.x) * (Q8_THREADS / 32) + (threadIdx.x >> 5);
-       i < total; i += step) {
-    const long long r = i / ng;
-    const long long c = (i - r * ng) * Q8_GROUP + lane;
-    const float v = c < cols ? Elem<T>::to(x[r * ld + c]) : 0.0f;
-    const uint32_t b = q8_scale_byte<FMT>(warp_max_u32(__float_as_uint(v) & 0x7fffffffu));
-    q[i * Q8_GROUP + lane] = static_cast<uint8_t>(q8_code<FMT>(v * q8_inv_scale(b)));
-    if (lane == 0) scale[i] = static_cast<uint8_t>(b);
+// Vector i of a (rows, nv) grid of vectors: FLAT when rows lie without gaps, so that i
+// alone addresses it; else row and column come from a division, 32-bit within a CTA's
+// tile, whose first vector's row and column are (row0, v0).
+struct VecAt {
+  long long row;
+  int v;
+};
+template <bool FLAT>
+__device__ __forceinline__ VecAt vec_at(long long i, long long row0, unsigned v0, unsigned off,
+                                        unsigned nv) {
+  VecAt a;
+  if (FLAT) {
+    a.row = 0;
+    a.v = 0;
+  } else {
+    const unsigned k = (v0 + off) / nv;
+    a.row = row0 + k;
+    a.v = static_cast<int>(v0 + off - k * nv);
   }
+  return a;
 }
 
-template <typename T, int FMT>
+template <typename T, bool VEC, bool FLAT>
 __global__ void __launch_bounds__(Q8_THREADS)
-    act_restore_kernel(const uint8_t* q, const uint8_t* scale, long long rows, long long cols,
-                       long long ng, T* x, long long ld) {
-  const int lane = threadIdx.x & 31;
-  const long long total = rows * ng;
-  const long long step = static_cast<long long>(gridDim.x) * (Q8_THREADS / 32);
-  for (long long i = static_cast<long long>(blockIdx.x) * (Q8_THREADS / 32) + (threadIdx.x >> 5);
-       i < total; i += step) {
-    const long long r = i / ng;
-    const long long c = (i - r * ng) * Q8_GROUP + lane;
-    if (c < cols)
-      x[r * ld + c] = Elem<T>::from(q8_value<FMT>(q[i * Q8_GROUP + lane]) * q8_scale(scale[i]));
-  }
-}
-
-// CTAs of a grid-strided launch over `items` warps' worth of work.
-static unsigned warp_grid(long long items) {
-  const long long need = (items + Q8_THREADS / 32 - 1) / (Q8_THREADS / 32);
-  const long long cap = static_cast<long long>(device_sm_count()) * 32;
-  return static_cast<unsigned>(need < cap ? need : (cap > 0 ? cap : 1));
-}
-
-template <typename T>
-static void compress_t(const CompressArgs& a, long long ng, unsigned grid, cudaStream_t st) {
+    act_compress_kernel(const CompressArgs a, unsigned nv, long long total) {
+  const long long base = static_cast<long long>(blockIdx.x) * (Q8_THREADS * Q8_U);
+  const long long row0 = FLAT ? 0 : base / nv;
+  const unsigned v0 = FLAT ? 0 : static_cast<unsigned>(base - row0 * nv);
   const T* x = static_cast<const T*>(a.x);
-  if (a.fmt == DASH_Q8_INT8)
-    act_compress_kernel<T, DASH_Q8_INT8>
-        <<<grid, Q8_THREADS, 0, st>>>(x, a.rows, a.cols, a.ld, ng, a.q, a.scale);
-  else
-    act_compress_kernel<T, DASH_Q8_E4M3>
-        <<<grid, Q8_THREADS, 0, st>>>(x, a.rows, a.cols, a.ld, ng, a.q, a.scale);
+  float v[Q8_U][8];
+#pragma unroll
+  for (int u = 0; u < Q8_U; ++u) {
+    const unsigned off = u * Q8_THREADS + threadIdx.x;
+    const long long i = base + off;
+    const VecAt at = vec_at<FLAT>(i, row0, v0, off, nv);
+    const int left = i >= total ? 0 : (FLAT ? 8 : static_cast<int>(min(a.cols - at.v * 8LL, 8LL)));
+    load8<T, VEC>(x + (FLAT ? i * 8 : at.row * a.ld + at.v * 8LL), left, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < Q8_U; ++u) {
+    const long long i = base + u * Q8_THREADS + threadIdx.x;
+    uint2 codes;
+    const uint32_t b = q8_encode8(a.fmt, group_amax(v[u]), v[u], codes);
+    if (i < total) {
+      // Codes lie without gaps whatever the matrix does.
+      reinterpret_cast<uint2*>(a.q)[i] = codes;
+      if ((threadIdx.x & 3) == 0) a.scale[i >> 2] = static_cast<uint8_t>(b);
+    }
+  }
+}
+
+template <typename T, bool VEC, bool FLAT>
+__global__ void __launch_bounds__(Q8_THREADS)
+    act_restore_kernel(const RestoreArgs a, unsigned nv, long long total) {
+  const long long base = static_cast<long long>(blockIdx.x) * (Q8_THREADS * Q8_U);
+  const long long row0 = FLAT ? 0 : base / nv;
+  const unsigned v0 = FLAT ? 0 : static_cast<unsigned>(base - row0 * nv);
+  T* x = static_cast<T*>(a.x);
+  uint2 codes[Q8_U];
+  uint32_t b[Q8_U];
+#pragma unroll
+  for (int u = 0; u < Q8_U; ++u) {
+    const long long i = base + u * Q8_THREADS + threadIdx.x;
+    codes[u] = make_uint2(0u, 0u);
+    b[u] = 127u;
+    if (i < total) {
+      codes[u] = reinterpret_cast<const uint2*>(a.q)[i];
+      b[u] = a.scale[i >> 2];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < Q8_U; ++u) {
+    const unsigned off = u * Q8_THREADS + threadIdx.x;
+    const long long i = base + off;
+    const VecAt at = vec_at<FLAT>(i, row0, v0, off, nv);
+    const int left = i >= total ? 0 : (FLAT ? 8 : static_cast<int>(min(a.cols - at.v * 8LL, 8LL)));
+    float v[8];
+    q8_decode8(a.fmt, codes[u], b[u], v);
+    store8<T, VEC>(x + (FLAT ? i * 8 : at.row * a.ld + at.v * 8LL), left, v);
+  }
+}
+
+// Access of a (rows, cols) matrix: eight-column vectors where address, leading dimension
+// and width allow them (2); without gaps between rows of whole groups besides (3); else
+// single elements (0).
+static int access_mode(const void* x, int dt, long long cols, long long ld) {
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && cols % 8 == 0 &&
+                   (ld * dt_bytes(dt)) % 16 == 0;
+  return vec ? (ld == cols && cols % Q8_GROUP == 0 ? 3 : 2) : 0;
 }
 
 template <typename T>
-static void restore_t(const RestoreArgs& a, long long ng, unsigned grid, cudaStream_t st) {
-  T* x = static_cast<T*>(a.x);
-  if (a.fmt == DASH_Q8_INT8)
-    act_restore_kernel<T, DASH_Q8_INT8>
-        <<<grid, Q8_THREADS, 0, st>>>(a.q, a.scale, a.rows, a.cols, ng, x, a.ld);
+static void compress_t(const CompressArgs& a, int mode, unsigned grid, unsigned nv,
+                       long long total, cudaStream_t st) {
+  if (mode == 3)
+    act_compress_kernel<T, true, true><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+  else if (mode == 2)
+    act_compress_kernel<T, true, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
   else
-    act_restore_kernel<T, DASH_Q8_E4M3>
-        <<<grid, Q8_THREADS, 0, st>>>(a.q, a.scale, a.rows, a.cols, ng, x, a.ld);
+    act_compress_kernel<T, false, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+}
+
+template <typename T>
+static void restore_t(const RestoreArgs& a, int mode, unsigned grid, unsigned nv,
+                      long long total, cudaStream_t st) {
+  if (mode == 3)
+    act_restore_kernel<T, true, true><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+  else if (mode == 2)
+    act_restore_kernel<T, true, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+  else
+    act_restore_kernel<T, false, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+}
+
+// Vectors of the padded matrix, and the CTAs that hold them; false where the grid cannot.
+static bool vec_grid(long long rows, long long cols, unsigned& nv, long long& total,
+                     unsigned& grid) {
+  nv = static_cast<unsigned>((cols + Q8_GROUP - 1) / Q8_GROUP * 4);
+  total = rows * nv;
+  const long long g = (total + Q8_THREADS * Q8_U - 1) / (Q8_THREADS * Q8_U);
+  grid = static_cast<unsigned>(g);
+  return g <= 0x7fffffff;
 }
 
 dash_status launch_act_compress(const CompressArgs& a, cudaStream_t st) {
-  const long long ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP;
-  const unsigned grid = warp_grid(a.rows * ng);
+  unsigned nv, grid;
+  long long total;
+  if (!vec_grid(a.rows, a.cols, nv, total, grid)) return DASH_ERR_UNSUPPORTED;
+  const int mode = access_mode(a.x, a.dt, a.cols, a.ld);
   const int rec = trace_begin(st);
   if (a.dt == DASH_DT_F32)
-    compress_t<float>(a, ng, grid, st);
+    compress_t<float>(a, mode, grid, nv, total, st);
   else if (a.dt == DASH_DT_BF16)
-    compress_t<__nv_bfloat16>(a, ng, grid, st);
+    compress_t<__nv_bfloat16>(a, mode, grid, nv, total, st);
   else
-    compress_t<__half>(a, ng, grid, st);
+    compress_t<__half>(a, mode, grid, nv, total, st);
   const cudaError_t err = cudaGetLastError();
   trace_end(rec, st, DASH_TRACE_CHECKPOINT, 0.0,
-            static_cast<double>(a.rows) * (a.cols * dt_bytes(a.dt) + ng * (Q8_GROUP + 1)));
+            static_cast<double>(a.rows) * (a.cols * dt_bytes(a.dt) + nv * 8.25));
   return err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 dash_status launch_act_restore(const RestoreArgs& a, cudaStream_t st) {
-  const long long ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP;
-  const unsigned grid = warp_grid(a.rows * ng);
+  unsigned nv, grid;
+  long long total;
+  if (!vec_grid(a.rows, a.cols, nv, total, grid)) return DASH_ERR_UNSUPPORTED;
+  const int mode = access_mode(a.x, a.dt, a.cols, a.ld);
   const int rec = trace_begin(st);
   if (a.dt == DASH_DT_F32)
-    restore_t<float>(a, ng, grid, st);
+    restore_t<float>(a, mode, grid, nv, total, st);
   else if (a.dt == DASH_DT_BF16)
-    restore_t<__nv_bfloat16>(a, ng, grid, st);
+    restore_t<__nv_bfloat16>(a, mode, grid, nv, total, st);
   else
-    restore_t<__half>(a, ng, grid, st);
+    restore_t<__half>(a, mode, grid, nv, total, st);
   const cudaError_t err = cudaGetLastError();
   trace_end(rec, st, DASH_TRACE_CHECKPOINT, 0.0,
-            static_cast<double>(a.rows) * (a.cols * dt_bytes(a.dt) + ng * (Q8_GROUP + 1)));
+            static_cast<double>(a.rows) * (a.cols * dt_bytes(a.dt) + nv * 8.25));
   return err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
