@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(Q8_THREADS)
   const long long row0 = FLAT ? 0 : base / nv;
   const unsigned v0 = FLAT ? 0 : static_cast<unsigned>(base - row0 * nv);
   const T* x = static_cast<const T*>(a.x);
-  float v[Q8_U][8];
+  F2 v[Q8_U][4];
 #pragma unroll
   for (int u = 0; u < Q8_U; ++u) {
     const unsigned off = u * Q8_THREADS + threadIdx.x;
@@ -89,8 +89,11 @@ __global__ void __launch_bounds__(Q8_THREADS)
     const long long i = base + off;
     const VecAt at = vec_at<FLAT>(i, row0, v0, off, nv);
     const int left = i >= total ? 0 : (FLAT ? 8 : static_cast<int>(min(a.cols - at.v * 8LL, 8LL)));
-    float v[8];
-    q8_decode8(a.fmt, codes[u], b[u], v);
+    F2 v[4];
+    if (a.fmt == DASH_Q8_INT8)
+      q8_decode8<DASH_Q8_INT8>(codes[u], b[u], v);
+    else
+      q8_decode8<DASH_Q8_E4M3>(codes[u], b[u], v);
     store8<T, VEC>(x + (FLAT ? i * 8 : at.row * a.ld + at.v * 8LL), left, v);
   }
 }

@@ -102,71 +102,143 @@ __device__ __forceinline__ float q8_value(uint32_t code) {
   return __half2float(__half(h));
 }
 
-// ---------------------------------------------------------------- eight at a time
-// A thread's unit of work is eight consecutive columns; four neighbouring lanes hold one
-// group.
+// ---------------------------------------------------------------- packed fp32 pairs
+// Two fp32 numbers in one 64-bit register, each operation on both in one instruction with
+// the rounding of the single one.  The norm and checkpoint kernels issue some ten
+// instructions per element with these and twice that without, and issue is what holds
+// them below HBM's rate for 16-bit types.
 
-// Eight elements from p, of which `n` (0 .. 8) exist; the others are zero.  VEC: p is
-// 16-byte aligned and n is 0 or 8.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void f2_get(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+  float lo, hi;
+  f2_get(a, lo, hi);
+  return lo + hi;
+}
+// max(m, |lo|, |hi|), NaN if one of them is.
+__device__ __forceinline__ float f2_amax(float m, F2 a) {
+  float lo, hi, r;
+  f2_get(a, lo, hi);
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(lo), "f"(hi));
+  return r;
+}
+
+// ---------------------------------------------------------------- eight at a time
+// A thread's unit of work is eight consecutive columns, four pairs; four neighbouring
+// lanes hold one group.
+
+// The two elements of a 32-bit word of a 16-bit type, and back (rounded once).
+template <typename T>
+__device__ __forceinline__ F2 unpack2(uint32_t w) {
+  if constexpr (Elem<T>::is_bf16) {
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return f2(f.x, f.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+  float lo, hi;
+  f2_get(a, lo, hi);
+  if constexpr (Elem<T>::is_bf16)
+    return pack_bf162(lo, hi);
+  else
+    return pack_half2(lo, hi);
+}
+
+// Eight elements from p, of which `n` exist (any n; <= 0: none); the others are zero.
+// VEC: p is 16-byte aligned and none or all of the eight exist.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* p, int n, F2 (&v)[4]) {
   if constexpr (!VEC) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? Elem<T>::to(p[k]) : 0.0f;
+    for (int k = 0; k < 4; ++k)
+      v[k] = f2(2 * k < n ? Elem<T>::to(p[2 * k]) : 0.0f,
+                2 * k + 1 < n ? Elem<T>::to(p[2 * k + 1]) : 0.0f);
   } else {
-    if (n <= 0) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-      return;
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+    if (n > 0) {
+      a = reinterpret_cast<const uint4*>(p)[0];
+      if constexpr (sizeof(T) == 4) b = reinterpret_cast<const uint4*>(p)[1];
     }
     if constexpr (sizeof(T) == 4) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0];
-      const float4 b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 2 && Elem<T>::is_bf16) {
-          v[2 * k] = __uint_as_float(w[k] << 16);
-          v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-          v[2 * k] = f.x;
-          v[2 * k + 1] = f.y;
-        }
-      }
+      v[0] = unpack2<T>(a.x);
+      v[1] = unpack2<T>(a.y);
+      v[2] = unpack2<T>(a.z);
+      v[3] = unpack2<T>(a.w);
     }
   }
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* p, int n, const F2 (&v)[4]) {
   if constexpr (!VEC) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = Elem<T>::from(v[k]);
+    for (int k = 0; k < 4; ++k) {
+      float lo, hi;
+      f2_get(v[k], lo, hi);
+      if (2 * k < n) p[2 * k] = Elem<T>::from(lo);
+      if (2 * k + 1 < n) p[2 * k + 1] = Elem<T>::from(hi);
+    }
   } else {
     if (n <= 0) return;
     if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if constexpr (Elem<T>::is_bf16) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf162(v[0], v[1]), pack_bf162(v[2], v[3]),
-                                                pack_bf162(v[4], v[5]), pack_bf162(v[6], v[7]));
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f2_get(v[k], f[2 * k], f[2 * k + 1]);
+      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     } else {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
-                                                pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack2<T>(v[0]), pack2<T>(v[1]), pack2<T>(v[2]), pack2<T>(v[3]));
     }
   }
 }
 
+// The value after a round trip through T.
+template <typename T>
+__device__ __forceinline__ F2 round2(F2 a) {
+  if constexpr (sizeof(T) == 4)
+    return a;
+  else
+    return unpack2<T>(pack2<T>(a));
+}
+
 // Eight elements of a per-column vector whose type is a run-time argument.  vec: the
-// vector is 16-byte aligned and n is 0 or 8.
+// vector is 16-byte aligned and none or all of the eight exist.
 __device__ __forceinline__ void load8_dt(const void* p, int dt, bool vec, int64_t i, int n,
-                                         float (&v)[8]) {
+                                         F2 (&v)[4]) {
   if (vec) {
     if (dt == DASH_DT_F32)
       load8<float, true>(static_cast<const float*>(p) + i, n, v);
@@ -177,61 +249,75 @@ __device__ __forceinline__ void load8_dt(const void* p, int dt, bool vec, int64_
     return;
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = k < n ? load_dt(p, dt, i + k) : 0.0f;
+  for (int k = 0; k < 4; ++k)
+    v[k] = f2(2 * k < n ? load_dt(p, dt, i + 2 * k) : 0.0f,
+              2 * k + 1 < n ? load_dt(p, dt, i + 2 * k + 1) : 0.0f);
 }
 
-// Largest magnitude bits of the group that this lane shares with its three neighbours.
-__device__ __forceinline__ uint32_t group_amax(const float (&v)[8]) {
-  uint32_t m = 0;
+// Largest magnitude (bits; NaN's are above infinity's) of the group that this lane shares
+// with its three neighbours.
+__device__ __forceinline__ uint32_t group_amax(const F2 (&v)[4]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  for (int k = 0; k < 4; ++k) m = f2_amax(m, v[k]);
+  uint32_t b = __float_as_uint(m) & 0x7fffffffu;
+  b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
+  return max(b, __shfl_xor_sync(0xffffffffu, b, 2));
 }
 
 // Scale byte and codes of eight values from their group's largest magnitude.
-__device__ __forceinline__ uint32_t q8_encode8(int fmt, uint32_t amax, const float (&v)[8],
+__device__ __forceinline__ uint32_t q8_encode8(int fmt, uint32_t amax, const F2 (&v)[4],
                                                uint2& codes) {
+  uint32_t w[4];
+  uint32_t b;
+  float lo, hi;
   if (fmt == DASH_Q8_INT8) {
-    const uint32_t b = q8_scale_byte<DASH_Q8_INT8>(amax);
-    const float inv = q8_inv_scale(b);
-    uint32_t c[8];
-    if (b == 121u + 127u) {
-      // The largest scale does not grow any further: saturate.
-#pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = q8_code<DASH_Q8_INT8>(v[k] * inv);
-    } else {
+    b = q8_scale_byte<DASH_Q8_INT8>(amax);
+    const F2 inv = f2(q8_inv_scale(b));
+    if (b != 121u + 127u) {
       // 1.5 2^23 + x holds x, rounded to nearest even, in its low byte; the product is
       // exact.
+      const F2 magic = f2(12582912.0f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = __float_as_uint(fmaf(v[k], inv, 12582912.0f));
+      for (int k = 0; k < 4; ++k) {
+        f2_get(f2_fma(v[k], inv, magic), lo, hi);
+        w[k] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
+      }
+    } else {
+      // The largest scale does not grow any further: saturate.
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f2_get(v[k] * inv, lo, hi);
+        w[k] = q8_code<DASH_Q8_INT8>(lo) | q8_code<DASH_Q8_INT8>(hi) << 8;
+      }
     }
-    codes.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-    codes.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-    return b;
-  }
-  const uint32_t b = q8_scale_byte<DASH_Q8_E4M3>(amax);
-  const float inv = q8_inv_scale(b);
-  uint32_t h[4];
+  } else {
+    b = q8_scale_byte<DASH_Q8_E4M3>(amax);
+    const F2 inv = f2(q8_inv_scale(b));
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    h[k] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * k] * inv, v[2 * k + 1] * inv),
-                                    __NV_SATFINITE, __NV_E4M3);
-  codes.x = h[0] | (h[1] << 16);
-  codes.y = h[2] | (h[3] << 16);
+    for (int k = 0; k < 4; ++k) {
+      f2_get(v[k] * inv, lo, hi);
+      w[k] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+  codes.x = __byte_perm(w[0], w[1], 0x5410);
+  codes.y = __byte_perm(w[2], w[3], 0x5410);
   return b;
 }
 
 // The values of eight codes.
-__device__ __forceinline__ void q8_decode8(int fmt, const uint2& codes, uint32_t byte,
-                                           float (&v)[8]) {
-  const float s = q8_scale(byte);
-  if (fmt == DASH_Q8_INT8) {
+template <int FMT>
+__device__ __forceinline__ void q8_decode8(const uint2& codes, uint32_t byte, F2 (&v)[4]) {
+  const F2 s = f2(q8_scale(byte));
+  if constexpr (FMT == DASH_Q8_INT8) {
     // 2^23 + (q + 128) from the code's byte, less 2^23 + 128.
+    const F2 less = f2(-8388736.0f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t u = (k < 4 ? codes.x : codes.y) ^ 0x80808080u;
-      v[k] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + (k & 3))) - 8388736.0f) * s;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u = (k < 2 ? codes.x : codes.y) ^ 0x80808080u;
+      const F2 f = f2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + 2 * (k & 1))),
+                      __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441 + 2 * (k & 1))));
+      v[k] = (f + less) * s;
     }
   } else {
 #pragma unroll
@@ -240,14 +326,9 @@ __device__ __forceinline__ void q8_decode8(int fmt, const uint2& codes, uint32_t
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
           static_cast<__nv_fp8x2_storage_t>((k & 1) ? w >> 16 : w & 0xffffu), __NV_E4M3);
       const float2 f = __half22float2(__half2(h));
-      v[2 * k] = f.x * s;
-      v[2 * k + 1] = f.y * s;
+      v[k] = f2(f.x, f.y) * s;
     }
   }
-}
-
-__device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) {
-  return __reduce_max_sync(0xffffffffu, v);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -300,9 +300,10 @@ dash_status dash_device_status(void) {
   const int c = power_tc_read_clear_error();
   const int d = power_cluster_read_clear_error();
   const int e = weight_grad_read_clear_error();
-  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0) return DASH_ERR_CUDA;
+  const int f = norm_read_clear_error();
+  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0) return DASH_ERR_CUDA;
   if (a == DASH_ERR_TIMEOUT || b == DASH_ERR_TIMEOUT || c == DASH_ERR_TIMEOUT ||
-      d == DASH_ERR_TIMEOUT || e == DASH_ERR_TIMEOUT)
+      d == DASH_ERR_TIMEOUT || e == DASH_ERR_TIMEOUT || f == DASH_ERR_TIMEOUT)
     return DASH_ERR_TIMEOUT;
   if (a == DASH_ERR_CONFLICT) return DASH_ERR_CONFLICT;
   return DASH_OK;

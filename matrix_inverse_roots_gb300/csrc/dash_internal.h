@@ -182,6 +182,7 @@ int power_tc_read_clear_error();
 int power_cluster_read_clear_error();
 int elementwise_read_clear_error();
 int weight_grad_read_clear_error();
+int norm_read_clear_error();
 
 int device_sm_count();
 

@@ -8,58 +8,89 @@
 
 namespace dash {
 
+int norm_read_clear_error() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_dash_error, sizeof(int)) != cudaSuccess) return -1;
+  if (cudaMemcpyToSymbol(g_dash_error, &z, sizeof(int)) != cudaSuccess) return -1;
+  return v;
+}
+
 // A row is held by W warps, J vectors of eight columns per thread: thread t of the row has
 // columns 8 (j 32 W + t).
 
-// Sums of N values over the W warps of a row (W = 1: one warp; else the whole CTA, or the
-// named barrier's group of warps), the same in every thread.  red holds N floats per warp.
+// Sums of N (1 or 2) values over the W warps of a row (W = 1: one warp; else the whole CTA,
+// or the named barrier's group of warps), the same in every thread.  red holds 32 floats
+// per value.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int W, int warp_in_row, float* red,
                                         int barrier) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (W == 1) return;
   const int lane = threadIdx.x & 31;
-  if (lane == 0)
+  if constexpr (N == 2) {
+    // The lower half-warp goes on with the first value, the upper with the second.
+    const bool up = lane >= 16;
+    float x = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i * 32 + warp_in_row] = v[i];
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (W == 1) {
+      v[0] = __shfl_sync(0xffffffffu, x, 0);
+      v[1] = __shfl_sync(0xffffffffu, x, 16);
+      return;
+    }
+    if ((lane & 15) == 0) red[(lane << 1) + warp_in_row] = x;
+  } else {
+    v[0] = warp_sum(v[0]);
+    if (W == 1) return;
+    if (lane == 0) red[warp_in_row] = v[0];
+  }
   asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(W * 32) : "memory");
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < W ? red[i * 32 + lane] : 0.0f);
+  for (int i = 0; i < N; ++i) {
+    if (W <= 8) {
+      // Up to eight partial sums: read by every thread, the missing ones as zeros.
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) t += w < W ? red[i * 32 + w] : 0.0f;
+      v[i] = t;
+    } else {
+      v[i] = warp_sum(lane < W ? red[i * 32 + lane] : 0.0f);
+    }
+  }
 }
 
-// Largest CTA of a forward instance: J vectors per thread and at most 2048 vectors a row.
-constexpr int fwd_threads(int J) { return J <= 2 ? 1024 : (J == 4 ? 512 : 256); }
+// Largest CTA of a forward instance: J vectors per thread, at most 2048 vectors a row.
+constexpr int fwd_threads(int J) { return J <= 2 ? 1024 : 512; }
 
-// The variance is taken about the mean, in a second pass over the registers.
+// W = 1: a row per warp, else a row per CTA; small CTAs, many per SM, cover one another's
+// loads and sums.  The variance is taken about the mean, in a second pass over the
+// registers.  (Measured and not taken: rows brought in by bulk copies several rows ahead,
+// by persistent CTAs.  36.3 against 32.2 us at 8192 x 2048 bf16 with residual and
+// checkpoint, since what bounds it is instruction issue, not the loads' latency.)
 template <typename T, int J, bool VEC>
 __global__ void __launch_bounds__(fwd_threads(J))
     norm_forward_kernel(const NormFwdArgs a, int W, bool wvec) {
   __shared__ float red[2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // W = 1: a row per warp; else a row per CTA.
   const long long row =
       W == 1 ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
   if (row >= a.rows) return;
   const int t = W == 1 ? lane : static_cast<int>(threadIdx.x);
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const T* res = static_cast<const T*>(a.residual) + row * a.ldres;
-  float v[J][8];
-  float s[1] = {0.0f};
+  F2 v[J][4];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (j * 32 * W + t) * 8;
     load8<T, VEC>(x + c, a.cols - c, v[j]);
   }
   if (a.residual) {
+    // The stream is carried in its own type: the norm sees the rounded sum.
+    const T* res = static_cast<const T*>(a.residual) + row * a.ldres;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int c = (j * 32 * W + t) * 8;
-      float u[8];
+      F2 u[4];
       load8<T, VEC>(res + c, a.cols - c, u);
-      // The stream is carried in its own type: the norm sees the rounded sum.
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = Elem<T>::to(Elem<T>::from(v[j][k] + u[k]));
+      for (int k = 0; k < 4; ++k) v[j][k] = round2<T>(v[j][k] + u[k]);
     }
   }
   if (a.r) {
@@ -70,26 +101,40 @@ __global__ void __launch_bounds__(fwd_threads(J))
       store8<T, VEC>(r + c, a.cols - c, v[j]);
     }
   }
+  float s[1];
   float mean = 0.0f;
   if (a.center) {
+    F2 p = f2(0.0f);
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[0] += v[j][k];
+      for (int k = 0; k < 4; ++k) p = p + v[j][k];
+    s[0] = f2_sum(p);
     row_sum<1>(s, W, warp, red[0], 0);
     mean = s[0] / a.cols;
-  }
-  s[0] = 0.0f;
+    const F2 less = f2(-mean);
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int n = a.cols - (j * 32 * W + t) * 8;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int j = 0; j < J; ++j) {
+      const int n = a.cols - (j * 32 * W + t) * 8;
       // Outside the row n stays 0, in the checkpoint's padding too.
-      v[j][k] = (VEC ? n > 0 : k < n) ? v[j][k] - mean : 0.0f;
-      s[0] = fmaf(v[j][k], v[j][k], s[0]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (VEC ? n > 0 : 2 * k + 1 < n) {
+          v[j][k] = v[j][k] + less;
+        } else if (!VEC && 2 * k < n) {
+          float lo, hi;
+          f2_get(v[j][k] + less, lo, hi);
+          v[j][k] = f2(lo, 0.0f);
+        }
+      }
     }
   }
+  F2 p = f2(0.0f);
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p = f2_fma(v[j][k], v[j][k], p);
+  s[0] = f2_sum(p);
   row_sum<1>(s, W, warp, red[1], 0);
   const float rstd = 1.0f / sqrtf(s[0] / a.cols + a.eps);
   if (t == 0) {
@@ -98,11 +143,12 @@ __global__ void __launch_bounds__(fwd_threads(J))
   }
   T* y = static_cast<T*>(a.y) + row * a.ldy;
   const int pitch = (a.cols + Q8_GROUP - 1) / Q8_GROUP * Q8_GROUP;
+  const F2 rs = f2(rstd);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (j * 32 * W + t) * 8;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[j][k] *= rstd;
+    for (int k = 0; k < 4; ++k) v[j][k] = v[j][k] * rs;
     if (a.q) {
       uint2 codes;
       const uint32_t b = q8_encode8(a.fmt, group_amax(v[j]), v[j], codes);
@@ -112,16 +158,16 @@ __global__ void __launch_bounds__(fwd_threads(J))
       }
     }
     if (c < a.cols) {
-      float w[8];
+      F2 w[4];
       if (a.gamma) {
         load8_dt(a.gamma, a.wdt, wvec, c, a.cols - c, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] *= w[k];
+        for (int k = 0; k < 4; ++k) v[j][k] = v[j][k] * w[k];
       }
       if (a.beta) {
         load8_dt(a.beta, a.wdt, wvec, c, a.cols - c, w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] += w[k];
+        for (int k = 0; k < 4; ++k) v[j][k] = v[j][k] + w[k];
       }
       store8<T, VEC>(y + c, a.cols - c, v[j]);
     }
@@ -132,159 +178,274 @@ __global__ void __launch_bounds__(fwd_threads(J))
 
 constexpr int BWD_WARPS = 16;
 
-// Eight elements as they lie in memory, so that a row waits in few registers between the
-// two times it is used.
-template <typename T, bool VEC>
-struct Raw8 {
-  alignas(16) T e[8];
-  __device__ __forceinline__ void load(const T* p, int n) {
-    if constexpr (!VEC) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = k < n ? p[k] : Elem<T>::from(0.0f);
-    } else if (n > 0) {
-      reinterpret_cast<uint4*>(e)[0] = reinterpret_cast<const uint4*>(p)[0];
-      if constexpr (sizeof(T) == 4)
-        reinterpret_cast<uint4*>(e)[1] = reinterpret_cast<const uint4*>(p)[1];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = Elem<T>::from(0.0f);
-    }
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = Elem<T>::to(e[k]);
-  }
-};
-
-// dx = rstd (g - mean(g) - n mean(g n)) + dres, g = dy gamma, and this CTA's share of
-// dgamma = sum dy n and dbeta = sum dy.  Persistent: a CTA of G groups of W warps, each
-// group a row at a time; a thread keeps its columns from row to row, so their sums stay in
-// registers and leave once, joined over the groups in shared memory, as row blockIdx.x of
-// `part` (dgamma's sums, then dbeta's).  CK: n from the checkpoint, else from x.
-template <typename T, bool CK, int J, bool VEC>
-__global__ void __launch_bounds__(32 * BWD_WARPS, 1)
-    norm_backward_kernel(const NormBwdArgs a, int W, int G, bool wvec, float* part) {
-  __shared__ float red[BWD_WARPS][2][2][32];
-  extern __shared__ float sums[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int grp = warp / W, wr = warp - grp * W;
-  const int t = wr * 32 + lane;
-  const int pitch = (a.cols + Q8_GROUP - 1) / Q8_GROUP * Q8_GROUP;
-  float dg[J][8], db[J][8];
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dg[j][k] = db[j][k] = 0.0f;
-  int flip = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * G + grp; row < a.rows;
-       row += static_cast<long long>(gridDim.x) * G) {
-    Raw8<T, VEC> dy[J], x[CK ? 1 : J];
-    uint2 q[CK ? J : 1];
-    uint32_t sc[CK ? J : 1];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = (j * 32 * W + t) * 8;
-      dy[j].load(static_cast<const T*>(a.dy) + row * a.lddy + c, a.cols - c);
-      if constexpr (CK) {
-        q[j] = make_uint2(0u, 0u);
-        sc[j] = 127u;
-        if (c < pitch) {
-          q[j] = *reinterpret_cast<const uint2*>(a.q + row * pitch + c);
-          sc[j] = a.scale[(row * pitch + c) / Q8_GROUP];
-        }
-      } else {
-        x[j].load(static_cast<const T*>(a.x) + row * a.ldx + c, a.cols - c);
-      }
-    }
-    const float rstd = a.rstd[row];
-    const float mean = (!CK && a.center) ? a.mean[row] : 0.0f;
-    auto norm8 = [&](int j, float (&n)[8]) {
-      if constexpr (CK) {
-        q8_decode8(a.fmt, q[j], sc[j], n);
-      } else {
-        x[j].get(n);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) n[k] = (n[k] - mean) * rstd;
-      }
-    };
-    auto grad8 = [&](int j, float (&d)[8], float (&g)[8]) {
-      const int c = (j * 32 * W + t) * 8;
-      dy[j].get(d);
-      if (a.gamma && c < a.cols) {
-        load8_dt(a.gamma, a.wdt, wvec, c, a.cols - c, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] *= d[k];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = d[k];
-      }
-    };
-    // Columns outside the row have dy = g = 0 and add nothing, whatever n is there (it is
-    // finite: the mean times rstd, or a padding code).
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if ((j * 32 * W + t) * 8 >= a.cols) continue;
-      float d[8], g[8], n[8];
-      norm8(j, n);
-      grad8(j, d, g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (!VEC && (j * 32 * W + t) * 8 + k >= a.cols) continue;
-        s[0] += g[k];
-        s[1] = fmaf(g[k], n[k], s[1]);
-        dg[j][k] = fmaf(d[k], n[k], dg[j][k]);
-        db[j][k] += d[k];
-      }
-    }
-    // Two buffers in turn: a row's sums may still be read when the next row's are written.
-    row_sum<2>(s, W, wr, red[grp][flip][0], 1 + grp);
-    flip ^= 1;
-    const float c1 = a.center ? s[0] / a.cols : 0.0f, c2 = s[1] / a.cols;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = (j * 32 * W + t) * 8;
-      if (c >= a.cols) continue;
-      float d[8], g[8], n[8];
-      norm8(j, n);
-      grad8(j, d, g);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = rstd * (g[k] - c1 - n[k] * c2);
-      if (a.dres) {
-        load8<T, VEC>(static_cast<const T*>(a.dres) + row * a.lddres + c, a.cols - c, d);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] += d[k];
-      }
-      store8<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx + c, a.cols - c, g);
-    }
-  }
-  if (part == nullptr) return;
-  float* out = part + static_cast<long long>(blockIdx.x) * 2 * a.cols;
-  // Group by group, in order.
+// Joins the groups' column sums, in order, into row blockIdx.x of `part` (dgamma's sums,
+// then dbeta's).  sums: 2 cols floats of shared memory.
+template <int J>
+__device__ __forceinline__ void join_groups(float* sums, float* part, int cols, int W, int G,
+                                            int grp, int t, const F2 (&dg)[J][4],
+                                            const F2 (&db)[J][4]) {
+  float* out = part + static_cast<long long>(blockIdx.x) * 2 * cols;
   for (int i = 0; i < G; ++i) {
     if (grp == i) {
+      float* to = i + 1 < G ? sums : out;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int c = (j * 32 * W + t) * 8;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (c + k >= a.cols) continue;
-          if (i > 0) {
-            dg[j][k] += sums[c + k];
-            db[j][k] += sums[a.cols + c + k];
-          }
-          if (i + 1 < G) {
-            sums[c + k] = dg[j][k];
-            sums[a.cols + c + k] = db[j][k];
-          } else {
-            out[c + k] = dg[j][k];
-            out[a.cols + c + k] = db[j][k];
+        for (int k = 0; k < 4; ++k) {
+          float g[2], b[2];
+          f2_get(dg[j][k], g[0], g[1]);
+          f2_get(db[j][k], b[0], b[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = c + 2 * k + h;
+            if (col >= cols) continue;
+            if (i > 0) {
+              g[h] += sums[col];
+              b[h] += sums[cols + col];
+            }
+            to[col] = g[h];
+            to[cols + col] = b[h];
           }
         }
       }
     }
     if (i + 1 < G) __syncthreads();
   }
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// W warps per row, G groups of them per CTA; with the ring, S stages of `stage` bytes for
+// each group.
+struct RowPlan {
+  int W, G, S;
+  uint32_t stage;
+};
+constexpr int RING_MAX = 8;                                 // most stages of a group
+constexpr int RING_BARS = 8 * BWD_WARPS * RING_MAX;         // their barriers
+
+// Where n comes from.
+enum NSource : int { N_FROM_X = 0, N_INT8 = 1, N_E4M3 = 2 };
+
+// dx = rstd (g - mean(g) - n mean(g n)) + dres, g = dy gamma, and this CTA's share of
+// dgamma = sum dy n and dbeta = sum dy.  Persistent, one CTA per SM: each group takes a row
+// at a time, and a thread keeps its columns from row to row, so that their sums stay in
+// registers and leave once, joined over the groups, as row blockIdx.x of `part`.
+// A row is read twice, before and after its sums.  (Held in registers in between it was
+// slower, 51.6 against 46.8 us at 8192 x 2048: the registers the sums leave are few.)
+// RING: a row's inputs come by bulk copies into a ring of shared-memory stages that the
+// group's first thread fills ahead, so that reads are in flight while a row's sums and
+// their barrier are waited for.  A stage is refilled once every thread has read it for the
+// last time, after the next row's barrier.  8192 x 2048 bf16 with int8 codes and dres: 58.5 us without,
+// 45.9 us with.  Without RING (rows of odd sizes or alignment, short or few rows) the
+// threads load for themselves.
+// After a wait that ran out the group carries on (its threads must meet at its barriers)
+// with whatever the stage holds and issues no more copies; the error flag tells.
+// Named barrier 1 + grp is the group's: barrier 0 is the whole CTA's, where groups that
+// have run out of rows wait while others still sum.
+template <typename T, int SRC, int J, bool VEC, bool RING>
+__global__ void __launch_bounds__(32 * BWD_WARPS, 1)
+    norm_backward_kernel(const NormBwdArgs a, const RowPlan p, bool wvec, float* part) {
+  constexpr bool CK = SRC != N_FROM_X;
+  __shared__ float red[BWD_WARPS][2][2 * 32];
+  __shared__ int abort_s;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = p.W, grp = warp / W, wr = warp - grp * W, t = wr * 32 + lane;
+  const bool first = t == 0;
+  const uint32_t bars = smem_u32(dyn) + 8u * (grp * p.S), data = smem_u32(dyn) + RING_BARS;
+  volatile int* abort_flag = &abort_s;
+  if (RING) {
+    if (threadIdx.x == 0) {
+      abort_s = 0;
+      for (int i = 0; i < p.G * p.S; ++i) mbar_init(smem_u32(dyn) + 8u * i, 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+  const long long step = static_cast<long long>(gridDim.x) * p.G;
+  const long long row0 = static_cast<long long>(blockIdx.x) * p.G + grp;
+  const int ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP, pitch = ng * Q8_GROUP;
+  const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  const uint32_t nbytes = CK ? static_cast<uint32_t>(pitch) : bytes;
+  // A stage: dy, x or the codes, dres.
+  auto fill = [&](long long row, int s) {
+    if (*abort_flag) return;
+    const uint32_t bar = bars + 8u * s;
+    const uint32_t dst = data + (grp * p.S + s) * p.stage;
+    mbar_arrive_expect_tx(bar, bytes + nbytes + (a.dres ? bytes : 0u));
+    bulk_load(dst, static_cast<const T*>(a.dy) + row * a.lddy, bytes, bar);
+    if (CK)
+      bulk_load(dst + bytes, a.q + row * pitch, nbytes, bar);
+    else
+      bulk_load(dst + bytes, static_cast<const T*>(a.x) + row * a.ldx, nbytes, bar);
+    if (a.dres)
+      bulk_load(dst + bytes + nbytes, static_cast<const T*>(a.dres) + row * a.lddres, bytes, bar);
+  };
+  if (RING && first)
+    for (int s = 0; s < p.S; ++s)
+      if (row0 + s * step < a.rows) fill(row0 + s * step, s);
+  // Up to two vectors' gamma stays in registers.
+  constexpr bool HOLD = J <= 2;
+  const int c0 = t * 8, cstep = 256 * W;  // columns c0 + j cstep
+  F2 gm[HOLD ? J : 1][4];
+  auto gamma8 = [&](int j, F2 (&g)[4]) {
+    const int c = c0 + j * cstep;
+    if (a.gamma) {
+      load8_dt(a.gamma, a.wdt, wvec, c, a.cols - c, g);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) g[k] = f2(1.0f);
+    }
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) gamma8(j, gm[j]);
+  }
+  F2 dg[J][4], db[J][4];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dg[j][k] = db[j][k] = f2(0.0f);
+  // Scales and statistics come straight from global memory, one row ahead; the pointers
+  // walk the group's rows.
+  constexpr int NSC = CK ? J : 1;
+  uint32_t sc[NSC] = {};
+  const uint8_t* scp = a.scale + (CK ? row0 * ng + t / 4 : 0);
+  const float* rsp = a.rstd + row0;
+  const float* mup = a.mean + row0;
+  float rstd = 0.0f, mean = 0.0f;
+  auto small = [&](uint32_t (&b)[NSC], float& rs, float& mu) {
+    if constexpr (CK) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) b[j] = c0 + j * cstep < pitch ? scp[j * (cstep / 32)] : 127u;
+      scp += step * ng;
+    } else if (a.center) {
+      mu = *mup;
+      mup += step;
+    }
+    rs = *rsp;
+    rsp += step;
+  };
+  if (row0 < a.rows) small(sc, rstd, mean);
+  const T* dyp = static_cast<const T*>(a.dy) + (RING ? 0 : row0 * a.lddy + c0);
+  const T* xp = static_cast<const T*>(a.x) + (RING || CK ? 0 : row0 * a.ldx + c0);
+  const uint8_t* qp = a.q + (RING || !CK ? 0 : row0 * pitch + c0);
+  const T* rp = static_cast<const T*>(a.dres) + (RING ? 0 : row0 * a.lddres + c0);
+  T* dxp = static_cast<T*>(a.dx) + row0 * a.lddx + c0;
+  const bool has_db = a.dbeta != nullptr;
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  for (long long row = row0; row < a.rows; row += step) {
+    uint32_t nsc[NSC] = {};
+    float nrstd = 0.0f, nmean = 0.0f;
+    if (row + step < a.rows) small(nsc, nrstd, nmean);
+    if (RING) {
+      mbar_wait(bars + 8u * s, ph, abort_flag);
+      const uint8_t* st = dyn + RING_BARS + (grp * p.S + s) * p.stage;
+      dyp = reinterpret_cast<const T*>(st) + c0;
+      xp = reinterpret_cast<const T*>(st + bytes) + c0;
+      qp = st + bytes + c0;
+      rp = reinterpret_cast<const T*>(st + bytes + nbytes) + c0;
+    }
+    const F2 rs = f2(rstd), less = f2(-mean);
+    // Vector j: dy and n.
+    auto vector8 = [&](int j, F2 (&d)[4], F2 (&m)[4]) {
+      const int left = a.cols - (c0 + j * cstep);
+      load8<T, VEC>(dyp + j * cstep, left, d);
+      if constexpr (CK) {
+        uint2 q = make_uint2(0u, 0u);
+        if (left > 0) q = *reinterpret_cast<const uint2*>(qp + j * cstep);
+        q8_decode8<SRC == N_INT8 ? DASH_Q8_INT8 : DASH_Q8_E4M3>(q, sc[j], m);
+      } else {
+        load8<T, VEC>(xp + j * cstep, left, m);
+        // The difference first: x may lie far from zero.
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = (m[k] + less) * rs;
+      }
+    };
+    auto scale8 = [&](int j, F2 (&d)[4]) {
+      F2 w[4];
+      if constexpr (!HOLD) gamma8(j, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = d[k] * (HOLD ? gm[HOLD ? j : 0][k] : w[k]);
+    };
+    F2 s1 = f2(0.0f), s2 = f2(0.0f);
+    // Columns outside the row have dy = g = 0 and add nothing to any sum: n is finite
+    // there (it is -mean rstd, or a padding code), unless the row is not finite anyway.
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (c0 + j * cstep >= a.cols) continue;
+      F2 gj[4], nj[4];
+      vector8(j, gj, nj);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dg[j][k] = f2_fma(gj[k], nj[k], dg[j][k]);
+        if (has_db) db[j][k] = db[j][k] + gj[k];
+      }
+      scale8(j, gj);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s1 = s1 + gj[k];
+        s2 = f2_fma(gj[k], nj[k], s2);
+      }
+    }
+    // The sums' buffers alternate: a slow warp may still read one row's when another
+    // writes the next row's.
+    float sum[2] = {f2_sum(s1), f2_sum(s2)};
+    row_sum<2>(sum, W, wr, red[grp][flip], 1 + grp);
+    flip ^= 1;
+    if (RING) {
+      if (W == 1) __syncwarp();
+      if (first && row != row0 && row + (p.S - 1) * step < a.rows)
+        fill(row + (p.S - 1) * step, s == 0 ? p.S - 1 : s - 1);
+    }
+    const F2 m1 = f2(a.center ? -(sum[0] / a.cols) : 0.0f), m2 = f2(-(sum[1] / a.cols));
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int left = a.cols - (c0 + j * cstep);
+      if (left <= 0) continue;
+      F2 gj[4], nj[4], rj[4];
+      vector8(j, gj, nj);
+      scale8(j, gj);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gj[k] = f2_fma(nj[k], m2, gj[k] + m1) * rs;
+      if (a.dres) {
+        load8<T, VEC>(rp + j * cstep, left, rj);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gj[k] = gj[k] + rj[k];
+      }
+      store8<T, VEC>(dxp + j * cstep, left, gj);
+    }
+    dxp += step * a.lddx;
+    if (RING) {
+      if (++s == p.S) {
+        s = 0;
+        ph ^= 1u;
+      }
+    } else {
+      dyp += step * a.lddy;
+      xp += step * a.ldx;
+      qp += step * pitch;
+      rp += step * a.lddres;
+    }
+#pragma unroll
+    for (int j = 0; j < NSC; ++j) sc[j] = nsc[j];
+    rstd = nrstd;
+    mean = nmean;
+  }
+  if (part == nullptr) return;
+  // Every copy has landed and been read: the groups' sums may overwrite the ring.
+  if (RING) __syncthreads();
+  join_groups<J>(reinterpret_cast<float*>(dyn), part, a.cols, W, p.G, grp, t, dg, db);
 }
 
 // ---------------------------------------------------------------- column sums
@@ -303,16 +464,16 @@ __global__ void __launch_bounds__(32 * CS_WARPS)
   const int n = static_cast<int>(cols - c < 8 ? cols - c : 8);
   const long long r0 = blockIdx.y * slice;
   const long long r1 = r0 + slice < rows ? r0 + slice : rows;
-  float s[8] = {};
+  F2 s[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
 #pragma unroll 8
   for (long long r = r0 + w; r < r1; r += CS_WARPS) {
-    float v[8];
+    F2 v[4];
     load8<T, VEC>(m + r * ld + c, n, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] += v[k];
+    for (int k = 0; k < 4; ++k) s[k] = s[k] + v[k];
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sb[w][lane * 8 + k] = s[k];
+  for (int k = 0; k < 4; ++k) f2_get(s[k], sb[w][lane * 8 + 2 * k], sb[w][lane * 8 + 2 * k + 1]);
   __syncthreads();
   const long long col = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (col < cols) {
@@ -323,36 +484,50 @@ __global__ void __launch_bounds__(32 * CS_WARPS)
   }
 }
 
+constexpr int PS_WARPS = 16;
+
 // out[y][c] = sum over p < parts of part[p][y][c], in a fixed order: lane x of warp w takes
-// p = w, w + 8, ...; the warps' sums are joined in order.
-__global__ void __launch_bounds__(256)
+// p = w, w + 16, ...; the warps' sums are joined in order.  Launched before the kernel that
+// writes `part` has ended (its launch latency then overlaps it) and waits for it here.
+__global__ void __launch_bounds__(32 * PS_WARPS)
     part_sum_kernel(const float* part, int parts, long long cols, long long stride, float* out0,
                     float* out1) {
-  __shared__ float sm[8][32];
+  __shared__ float sm[PS_WARPS][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
   float* out = blockIdx.y ? out1 : out0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (out == nullptr) return;
   const float* p0 = part + blockIdx.y * cols + c;
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 4
-    for (int p = w; p < parts; p += 8) s += p0[p * stride];
+#pragma unroll 8
+    for (int p = w; p < parts; p += PS_WARPS) s += p0[p * stride];
   }
   sm[w][lane] = s;
   __syncthreads();
   if (w == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sm[i][lane];
+    for (int i = 1; i < PS_WARPS; ++i) s += sm[i][lane];
     out[c] = s;
   }
 }
 
 static dash_status part_sum(const float* part, int parts, long long cols, long long stride,
                             float* out0, float* out1, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((cols + 31) / 32), out1 ? 2 : 1);
-  part_sum_kernel<<<grid, 256, 0, st>>>(part, parts, cols, stride, out0, out1);
-  return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((cols + 31) / 32), out1 ? 2 : 1);
+  cfg.blockDim = dim3(32 * PS_WARPS);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, part_sum_kernel, part, parts, cols, stride, out0, out1) ==
+                 cudaSuccess
+             ? DASH_OK
+             : DASH_ERR_CUDA;
 }
 
 // Slices of the rows: four CTAs per SM, each warp of one with 16 rows or more.
@@ -404,12 +579,12 @@ static dash_status forward_t(const NormFwdArgs& a, bool wvec, cudaStream_t st) {
   const int nvec = (a.cols + 7) / 8;
   // Vectors per thread: as many as leave some 16 warps per SM; fewer rows take more
   // threads each, for the latency of one row.
-  int J = 8;
+  int J = 4;
   while (J > 1 && (nvec <= 16 * J ||
                    static_cast<double>(a.rows) * ((nvec + 32 * J - 1) / (32 * J)) < 152 * 16))
     J /= 2;
   while ((nvec + 32 * J - 1) / (32 * J) > 32) J *= 2;
-  if (!VEC) J = 4;
+  if (!VEC) J = 2;
   const int W = (nvec + 32 * J - 1) / (32 * J);
   const int warps = W > 1 ? W : (a.rows < 152 * 4 ? 1 : 4);
   const long long grid = W > 1 ? a.rows : (a.rows + warps - 1) / warps;
@@ -419,12 +594,10 @@ static dash_status forward_t(const NormFwdArgs& a, bool wvec, cudaStream_t st) {
       norm_forward_kernel<T, 1, true><<<g, b, 0, st>>>(a, W, wvec);
     else if (J == 2)
       norm_forward_kernel<T, 2, true><<<g, b, 0, st>>>(a, W, wvec);
-    else if (J == 4)
-      norm_forward_kernel<T, 4, true><<<g, b, 0, st>>>(a, W, wvec);
     else
-      norm_forward_kernel<T, 8, true><<<g, b, 0, st>>>(a, W, wvec);
+      norm_forward_kernel<T, 4, true><<<g, b, 0, st>>>(a, W, wvec);
   } else {
-    norm_forward_kernel<T, 4, false><<<g, b, 0, st>>>(a, W, wvec);
+    norm_forward_kernel<T, 2, false><<<g, b, 0, st>>>(a, W, wvec);
   }
   return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
@@ -450,8 +623,9 @@ dash_status launch_norm_forward(const NormFwdArgs& a, cudaStream_t st) {
   return s;
 }
 
-// How a backward pass is laid out: J vectors per thread, W warps per row, G rows at once
-// per CTA, and one persistent CTA per SM.
+// How a backward pass is laid out: J vectors per thread (as few as the row's warps allow,
+// for the registers of its sums), W warps per row, G rows at once per CTA, one persistent
+// CTA per SM.
 struct BwdPlan {
   int J, W, G, grid;
 };
@@ -473,39 +647,55 @@ size_t norm_backward_ws(long long rows, long long cols) {
   return static_cast<size_t>(2) * bwd_plan(rows, cols).grid * cols * sizeof(float);
 }
 
-template <typename T, bool CK, int J, bool VEC>
-static dash_status backward_k(const NormBwdArgs& a, const BwdPlan& p, bool wvec, float* part,
-                              cudaStream_t st) {
-  auto k = norm_backward_kernel<T, CK, J, VEC>;
-  const size_t smem = p.G > 1 && part ? static_cast<size_t>(a.cols) * 8 : 0;
+template <typename T, int SRC, int J, bool VEC, bool RING>
+static dash_status backward_k(const NormBwdArgs& a, const BwdPlan& b, const RowPlan& p, bool wvec,
+                              float* part, cudaStream_t st) {
+  auto k = norm_backward_kernel<T, SRC, J, VEC, RING>;
+  size_t smem = RING ? static_cast<size_t>(p.G) * p.S * p.stage + RING_BARS : 0;
+  const size_t join = part && p.G > 1 ? static_cast<size_t>(a.cols) * 8 : 0;
+  if (smem < join) smem = join;
   if (smem > 32 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)) != cudaSuccess)
     return DASH_ERR_CUDA;
-  k<<<p.grid, 32 * p.W * p.G, smem, st>>>(a, p.W, p.G, wvec, part);
+  k<<<b.grid, 32 * p.W * p.G, smem, st>>>(a, p, wvec, part);
   return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
-template <typename T, bool CK>
-static dash_status backward_t(const NormBwdArgs& a, const BwdPlan& p, float* part,
+template <typename T, int SRC, int J>
+static dash_status backward_j(const NormBwdArgs& a, const BwdPlan& b, float* part,
                               cudaStream_t st) {
   const bool vec = a.cols % 8 == 0 && vec_ok(a.dy, a.lddy, a.dt) && vec_ok(a.dx, a.lddx, a.dt) &&
                    (!a.x || vec_ok(a.x, a.ldx, a.dt)) &&
                    (!a.dres || vec_ok(a.dres, a.lddres, a.dt));
   const bool wvec = a.cols % 8 == 0 && vec_ok(a.gamma, 0, a.wdt);
-  if (p.J == 4)
-    return vec ? backward_k<T, CK, 4, true>(a, p, wvec, part, st)
-               : backward_k<T, CK, 4, false>(a, p, wvec, part, st);
-  if (p.J == 2)
-    return vec ? backward_k<T, CK, 2, true>(a, p, wvec, part, st)
-               : backward_k<T, CK, 2, false>(a, p, wvec, part, st);
-  return vec ? backward_k<T, CK, 1, true>(a, p, wvec, part, st)
-             : backward_k<T, CK, 1, false>(a, p, wvec, part, st);
+  // The ring pays where every group has several rows of a KB or more, and needs two stages.
+  const size_t row = static_cast<size_t>(a.cols) * sizeof(T);
+  const size_t stage = row * (a.dres ? 2 : 1) +
+                       (SRC != N_FROM_X ? (a.cols + Q8_GROUP - 1) / Q8_GROUP * Q8_GROUP : row);
+  const size_t fit = (208 * 1024 - RING_BARS) / (stage * b.G);
+  RowPlan p = {b.W, b.G, 1, 0};
+  if (!vec) return backward_k<T, SRC, J, false, false>(a, b, p, wvec, part, st);
+  if (fit < 2 || stage < 1024 || a.rows < 152LL * b.G * 2)
+    return backward_k<T, SRC, J, true, false>(a, b, p, wvec, part, st);
+  p.S = static_cast<int>(fit < RING_MAX ? fit : RING_MAX);
+  p.stage = static_cast<uint32_t>(stage);
+  return backward_k<T, SRC, J, true, true>(a, b, p, wvec, part, st);
+}
+
+template <typename T, int SRC>
+static dash_status backward_t(const NormBwdArgs& a, const BwdPlan& b, float* part,
+                              cudaStream_t st) {
+  return b.J == 4   ? backward_j<T, SRC, 4>(a, b, part, st)
+         : b.J == 2 ? backward_j<T, SRC, 2>(a, b, part, st)
+                    : backward_j<T, SRC, 1>(a, b, part, st);
 }
 
 template <typename T>
 static dash_status backward_c(const NormBwdArgs& a, const BwdPlan& p, float* part,
                               cudaStream_t st) {
-  return a.q ? backward_t<T, true>(a, p, part, st) : backward_t<T, false>(a, p, part, st);
+  if (a.q == nullptr) return backward_t<T, N_FROM_X>(a, p, part, st);
+  return a.fmt == DASH_Q8_INT8 ? backward_t<T, N_INT8>(a, p, part, st)
+                               : backward_t<T, N_E4M3>(a, p, part, st);
 }
 
 dash_status launch_norm_backward(const NormBwdArgs& a, void* ws, cudaStream_t st) {
