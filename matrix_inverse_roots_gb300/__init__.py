@@ -207,10 +207,6 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream():
-    return torch.cuda.current_stream().cuda_stream
-
-
 def _stack(t, name, dtype=torch.float32):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
@@ -627,41 +623,69 @@ def _fmt(fmt):
     return Q8_FORMATS[fmt]
 
 
-def _rows(t, name, dtype=None, shape=None):
-    """A (rows, cols) matrix with unit column stride on the current device: (ld, dtype
-    code).  Rows may lie further apart than cols, not closer."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
-        raise TypeError("%s must be a 2-D CUDA tensor" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s but the current CUDA device is cuda:%d" % (
-            name, t.device, torch.cuda.current_device()))
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, (rows, cols)))
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+
+# These calls are short, so the binding counts: the checks below ask each tensor as little
+# as they can, and say what is wrong only once something is.
+
+
+def _begin():
+    """(library, current device, its current stream)."""
+    dev = torch.cuda.current_device()
+    return _lib or load_library(), dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _refuse(t, name, dev, what):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s but the current CUDA device is cuda:%d"
+                         % (name, t.device, dev))
+    raise what
+
+
+def _rows(t, name, dev, dtype=None, shape=None):
+    """Checks a (rows, cols) matrix with unit column stride on device `dev` and returns its
+    leading dimension.  Rows may lie further apart than cols, not closer."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dim() != 2:
+        _refuse(t, name, dev, TypeError("%s must be a 2-D CUDA tensor" % name))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(size)))
     ld, unit = t.stride()
+    cols = size[1]
     if unit != 1 and cols > 1:
         raise ValueError("%s must have unit column stride" % name)
     if ld < cols:
-        if rows > 1:
+        if size[0] > 1:
             raise ValueError("the rows of %s overlap" % name)
         ld = cols
-    return ld, _DTYPES.get(t.dtype, -1)
+    return ld
 
 
-_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+def _vec(t, name, dev, n, dtype=None):
+    """Checks a contiguous vector of n elements and returns its address."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dim() != 1
+            or t.shape[0] != n or not t.is_contiguous()):
+        _refuse(t, name, dev, ValueError("%s must be a contiguous vector of %d elements"
+                                         % (name, n)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    return t.data_ptr()
 
 
-def _vec(t, n, name, dtype=None):
-    _stack(t, name, dtype or t.dtype)
-    return _shape(t, (n,), name)
-
-
-def _codes(q, scale, rows, cols):
+def _codes(q, scale, dev, rows, cols):
+    """Checks a checkpoint of a (rows, cols) matrix."""
     ng = -(-cols // Q8_GROUP)
-    _shape(_stack(q, "q", torch.uint8), (rows, ng * Q8_GROUP), "q")
-    _shape(_stack(scale, "scale", torch.uint8), (rows, ng), "scale")
+    for t, name, shape in ((q, "q", (rows, ng * Q8_GROUP)), (scale, "scale", (rows, ng))):
+        if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.shape != shape
+                or not t.is_contiguous()):
+            _refuse(t, name, dev, ValueError("%s must be contiguous with shape %s"
+                                             % (name, shape)))
+        if t.dtype != torch.uint8:
+            raise TypeError("%s must be torch.uint8, got %s" % (name, t.dtype))
 
 
 def _empty_codes(rows, cols, device):
@@ -670,37 +694,53 @@ def _empty_codes(rows, cols, device):
             torch.empty((rows, ng), dtype=torch.uint8, device=device))
 
 
+def _norm_weights(gamma, beta, dev, cols):
+    """Addresses of gamma and beta and the code of the dtype they share."""
+    if gamma is None and beta is None:
+        return None, None, DT_F32
+    g = None if gamma is None else _vec(gamma, "gamma", dev, cols)
+    b = None if beta is None else _vec(beta, "beta", dev, cols,
+                                       None if gamma is None else gamma.dtype)
+    return g, b, _gdt(beta if gamma is None else gamma)
+
+
 def act_compress(x, fmt="int8", q=None, scale=None):
     """The 8-bit checkpoint of a matrix x (rows, cols): (q, scale), uint8 tensors of
     (rows, 32 G) codes and (rows, G) scale bytes, G = ceil(cols / 32).  fmt: "int8" or
     "e4m3".  x may be a row-strided view."""
-    lib = load_library()
     f = _fmt(fmt)
-    ld, dt = _rows(x, "x")
+    lib, dev, st = _begin()
+    ld = _rows(x, "x", dev)
     rows, cols = x.shape
     if q is None and scale is None:
         q, scale = _empty_codes(rows, cols, x.device)
     else:
-        _codes(q, scale, rows, cols)
-    _check(lib.act_compress(x.data_ptr(), dt, rows, cols, ld, f, q.data_ptr(), scale.data_ptr(),
-                            _raw_stream()), "act_compress")
+        _codes(q, scale, dev, rows, cols)
+    e = lib.act_compress(x.data_ptr(), _DTYPES.get(x.dtype, -1), rows, cols, ld, f, q.data_ptr(),
+                         scale.data_ptr(), st)
+    if e:
+        _check(e, "act_compress")
     return q, scale
 
 
 def act_restore(q, scale, cols, fmt="int8", dtype=torch.bfloat16, out=None):
     """The values of a checkpoint, (rows, cols) in `dtype`; `out` may be a row-strided view
     (its dtype is then the one written)."""
-    lib = load_library()
     f = _fmt(fmt)
+    lib, dev, st = _begin()
     if not isinstance(scale, torch.Tensor) or scale.dim() != 2:
         raise ValueError("scale must be a (rows, G) tensor")
     rows = scale.shape[0]
-    _codes(q, scale, rows, cols)
+    _codes(q, scale, dev, rows, cols)
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype, device=q.device)
-    ld, dt = _rows(out, "out", None, (rows, cols))
-    _check(lib.act_restore(q.data_ptr(), scale.data_ptr(), f, rows, cols, out.data_ptr(), dt, ld,
-                           _raw_stream()), "act_restore")
+        ld = cols
+    else:
+        ld = _rows(out, "out", dev, None, (rows, cols))
+    e = lib.act_restore(q.data_ptr(), scale.data_ptr(), f, rows, cols, out.data_ptr(),
+                        _DTYPES.get(out.dtype, -1), ld, st)
+    if e:
+        _check(e, "act_restore")
     return out
 
 
@@ -716,42 +756,46 @@ def layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, center=True, residual
     Returns NormForward(y, mean, rstd, r, q, scale): mean (None without center) and rstd if
     stats, r if a residual is given, q and scale (n's checkpoint) if ckpt is "int8" or
     "e4m3".  gamma and beta share a dtype.  r may be x or residual (in place)."""
-    lib = load_library()
-    ldx, dt = _rows(x, "x")
-    rows, cols = x.shape
-    dev, shape = x.device, (rows, cols)
-    wdt = DT_F32
-    if gamma is not None:
-        wdt = _gdt(_vec(gamma, cols, "gamma"))
-    if beta is not None:
-        wdt = _gdt(_vec(beta, cols, "beta", None if gamma is None else gamma.dtype))
+    lib, dev, st = _begin()
+    ldx = _rows(x, "x", dev)
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
+    g, b, wdt = _norm_weights(gamma, beta, dev, cols)
     ldres = ldr = 0
+    ldy = cols
     if residual is not None:
-        ldres, _ = _rows(residual, "residual", x.dtype, shape)
+        ldres = _rows(residual, "residual", dev, dtype, shape)
         if r is None:
-            r = torch.empty(shape, dtype=x.dtype, device=dev)
-    if r is not None:
-        ldr, _ = _rows(r, "r", x.dtype, shape)
+            r = torch.empty(shape, dtype=dtype, device=x.device)
+            ldr = cols
+    if r is not None and ldr == 0:
+        ldr = _rows(r, "r", dev, dtype, shape)
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
-    ldy, _ = _rows(y, "y", x.dtype, shape)
-    mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats and center else None
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
-    q = scale = None
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    else:
+        ldy = _rows(y, "y", dev, dtype, shape)
+    mean = rstd = q = scale = None
+    if stats:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if center:
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
     f = Q8_INT8
     if ckpt is not None:
         f = _fmt(ckpt)
-        q, scale = _empty_codes(rows, cols, dev)
-    _check(lib.layer_norm_forward(x.data_ptr(), ldx, _addr(residual), ldres, dt, rows, cols,
-                                  _addr(gamma), _addr(beta), wdt, eps, 1 if center else 0,
-                                  _addr(r), ldr, y.data_ptr(), ldy, _addr(mean), _addr(rstd), f,
-                                  _addr(q), _addr(scale), _raw_stream()), "layer_norm_forward")
+        q, scale = _empty_codes(rows, cols, x.device)
+    e = lib.layer_norm_forward(x.data_ptr(), ldx, _addr(residual), ldres, _DTYPES.get(dtype, -1),
+                               rows, cols, g, b, wdt, eps, 1 if center else 0, _addr(r), ldr,
+                               y.data_ptr(), ldy, _addr(mean), _addr(rstd), f, _addr(q),
+                               _addr(scale), st)
+    if e:
+        _check(e, "layer_norm_forward")
     return NormForward(y, mean, rstd, r, q, scale)
 
 
 def layer_norm_workspace_size(rows, cols):
+    """Workspace bytes of layer_norm_backward."""
     out = ctypes.c_size_t(0)
-    _check(load_library().dash_layer_norm_workspace_size(int(rows), int(cols), ctypes.byref(out)),
+    _check(load_library().dash_layer_norm_workspace_size(rows, cols, ctypes.byref(out)),
            "dash_layer_norm_workspace_size")
     return out.value
 
@@ -764,44 +808,46 @@ def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=N
     norm's input x (the forward's r), mean and rstd.  dres, the gradient that bypasses the
     norm, is added to dx.  dgamma is None without gamma, dbeta with beta=False; both are
     fp32.  dx may be dy or dres (in place)."""
-    lib = load_library()
-    lddy, dt = _rows(dy, "dy")
-    rows, cols = dy.shape
-    dev, shape = dy.device, (rows, cols)
-    _vec(rstd, rows, "rstd", torch.float32)
     f = _fmt(fmt)
+    lib, dev, st = _begin()
+    lddy = _rows(dy, "dy", dev)
+    shape, dtype = dy.shape, dy.dtype
+    rows, cols = shape
+    ps = _vec(rstd, "rstd", dev, rows, torch.float32)
     ldx = lddres = 0
+    pm = None
     if (x is None) == (q is None):
         raise ValueError("give the norm's input x or its checkpoint (q, scale), not both")
     if q is not None:
-        _codes(q, scale, rows, cols)
-        mean = None
+        _codes(q, scale, dev, rows, cols)
     else:
-        ldx, _ = _rows(x, "x", dy.dtype, shape)
+        ldx = _rows(x, "x", dev, dtype, shape)
         if center:
             if mean is None:
                 raise ValueError("mean is needed with x and center")
-            _vec(mean, rows, "mean", torch.float32)
-    wdt = DT_F32
+            pm = _vec(mean, "mean", dev, rows, torch.float32)
+    g, _, wdt = _norm_weights(gamma, None, dev, cols)
     dgamma = dbeta = None
     if gamma is not None:
-        wdt = _gdt(_vec(gamma, cols, "gamma"))
-        dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
     if beta:
-        dbeta = torch.empty(cols, dtype=torch.float32, device=dev)
+        dbeta = torch.empty(cols, dtype=torch.float32, device=dy.device)
     if dres is not None:
-        lddres, _ = _rows(dres, "dres", dy.dtype, shape)
+        lddres = _rows(dres, "dres", dev, dtype, shape)
     if dx is None:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dev)
-    lddx, _ = _rows(dx, "dx", dy.dtype, shape)
+        dx = torch.empty(shape, dtype=dtype, device=dy.device)
+        lddx = cols
+    else:
+        lddx = _rows(dx, "dx", dev, dtype, shape)
     if ws is None and (gamma is not None or beta):
         ws = torch.empty(max(layer_norm_workspace_size(rows, cols), 256), dtype=torch.uint8,
-                         device=dev)
-    _check(lib.layer_norm_backward(dy.data_ptr(), lddy, dt, rows, cols, _addr(x), ldx, _addr(mean),
-                                   _addr(q), _addr(scale), f, rstd.data_ptr(), _addr(gamma), wdt,
-                                   1 if center else 0, _addr(dres), lddres, dx.data_ptr(), lddx,
-                                   _addr(dgamma), _addr(dbeta), _addr(ws), _nbytes(ws),
-                                   _raw_stream()), "layer_norm_backward")
+                         device=dy.device)
+    e = lib.layer_norm_backward(dy.data_ptr(), lddy, _DTYPES.get(dtype, -1), rows, cols, _addr(x),
+                                ldx, pm, _addr(q), _addr(scale), f, ps, g, wdt,
+                                1 if center else 0, _addr(dres), lddres, dx.data_ptr(), lddx,
+                                _addr(dgamma), _addr(dbeta), _addr(ws), _nbytes(ws), st)
+    if e:
+        _check(e, "layer_norm_backward")
     return dx, dgamma, dbeta
 
 
@@ -821,35 +867,31 @@ def weight_grad(dz, q, scale, cols, fmt="int8", gamma=None, beta=None, B=None, d
     checkpoint of n: dW = dz^T (n gamma + beta), db = the column sums of dz (fp32; None
     unless bias).  dW has `dtype` (dz's by default) and is (outs, cols), or with B the
     zero-padded row-block-major (N, B, B) blocks of it, as pack_blocks cuts them."""
-    lib = load_library()
     f = _fmt(fmt)
-    lddz, dt = _rows(dz, "dz")
+    lib, dev, st = _begin()
+    lddz = _rows(dz, "dz", dev)
     rows, outs = dz.shape
-    dev = dz.device
-    _codes(q, scale, rows, cols)
-    wdt = DT_F32
-    if gamma is not None:
-        wdt = _gdt(_vec(gamma, cols, "gamma"))
-    if beta is not None:
-        wdt = _gdt(_vec(beta, cols, "beta", None if gamma is None else gamma.dtype))
-    b = int(B or 0)
+    _codes(q, scale, dev, rows, cols)
+    g, b, wdt = _norm_weights(gamma, beta, dev, cols)
+    B = int(B or 0)
+    shape = (-(-outs // B) * -(-cols // B), B, B) if B > 0 else (outs, cols)
+    ldw = cols
     if out is None:
-        dtype = dtype or dz.dtype
-        shape = (outs, cols) if not b else (-(-outs // b) * -(-cols // b), b, b)
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    if b:
-        _shape(_stack(out, "out", out.dtype), (-(-outs // b) * -(-cols // b), b, b), "out")
-        ldw = 0
+        out = torch.empty(shape, dtype=dtype or dz.dtype, device=dz.device)
+    elif B:
+        _shape(_stack(out, "out", out.dtype), shape, "out")
     else:
-        ldw, _ = _rows(out, "out", None, (outs, cols))
-    db = torch.empty(outs, dtype=torch.float32, device=dev) if bias else None
+        ldw = _rows(out, "out", dev, None, shape)
+    db = torch.empty(outs, dtype=torch.float32, device=dz.device) if bias else None
+    pz = dz.data_ptr()
     if ws is None:
-        ld = 0 if dz.data_ptr() & 15 else lddz
-        ws = torch.empty(max(weight_grad_workspace_size(rows, outs, cols, dz.dtype, b, ld), 256),
-                         dtype=torch.uint8, device=dev)
-    _check(lib.weight_grad(dz.data_ptr(), dt, lddz, rows, outs, q.data_ptr(), scale.data_ptr(), f,
-                           cols, _addr(gamma), _addr(beta), wdt, out.data_ptr(), _gdt(out), ldw, b,
-                           _addr(db), ws.data_ptr(), _nbytes(ws), _raw_stream()), "weight_grad")
+        n = weight_grad_workspace_size(rows, outs, cols, dz.dtype, B, 0 if pz & 15 else lddz)
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dz.device)
+    e = lib.weight_grad(pz, _DTYPES.get(dz.dtype, -1), lddz, rows, outs, q.data_ptr(),
+                        scale.data_ptr(), f, cols, g, b, wdt, out.data_ptr(), _gdt(out), ldw, B,
+                        _addr(db), ws.data_ptr(), _nbytes(ws), st)
+    if e:
+        _check(e, "weight_grad")
     return out, db
 
 
