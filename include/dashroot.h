@@ -534,7 +534,9 @@ dash_status dash_layer_norm_workspace_size(int64_t rows, int64_t cols, size_t* b
  * (ceil(outs / B) * ceil(cols / B), B, B) stack that pack_blocks would make of it
  * (B as for every stack; ldw ignored).  gamma, beta and db (outs,) fp32 may be NULL.
  * rows = 0 gives zeros; outs or cols = 0 is a no-op.  The products are exact (n is bf16,
- * and dz enters as one, two or three bf16 parts that add up to it), sums are fp32.
+ * and dz enters as one, two or three bf16 parts that add up to it), sums are fp32; where
+ * dz or dW is fp32 they are as accurate as a plain fp32 product's, else their error (about
+ * rows / 64 units in the last place of fp32) is far below the rounding of dW.
  * A stack dW is 16-byte aligned.
  * Workspace: dash_weight_grad_workspace_size, with the lddz of a dz whose address is a
  * multiple of 16 bytes, or 0 for any other dz (its parts are then laid out in the
@@ -546,7 +548,7 @@ dash_status weight_grad(const void* dz, int dt, int64_t lddz, int64_t rows, int6
                         const void* gamma, const void* beta, int wdt, void* dW, int odt,
                         int64_t ldw, int B, float* db, void* ws, size_t ws_bytes, void* stream);
 dash_status dash_weight_grad_workspace_size(int64_t rows, int64_t outs, int64_t cols, int dt,
-                                            int64_t lddz, int B, size_t* bytes);
+                                            int odt, int64_t lddz, int B, size_t* bytes);
 
 /* Workspace bytes for op on N blocks of order B (param: iters for CN/NDB,
  * degree for Chebyshev, n_vec for spectral_scale; gdt for accumulate/apply is

@@ -134,7 +134,7 @@ def load_library(path=None):
     lib.dash_layer_norm_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
     lib.weight_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, vp, vp, i32, vp, i32,
                                 i64, i32, vp, vp, sz, vp]
-    lib.dash_weight_grad_workspace_size.argtypes = [i64, i64, i64, i32, i64, i32,
+    lib.dash_weight_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, i64, i32,
                                                     ctypes.POINTER(sz)]
     lib.dash_gemm.argtypes = [vp, vp, i32, vp, vp, i32, i64, i32, i32, vp, vp]
     lib.dash_workspace_size.argtypes = [i32, i64, i32, i32, i32, ctypes.POINTER(sz)]
@@ -851,13 +851,15 @@ def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=N
     return dx, dgamma, dbeta
 
 
-def weight_grad_workspace_size(rows, outs, cols, dtype=torch.bfloat16, B=None, lddz=0):
-    """Workspace bytes of weight_grad.  lddz: the row stride of a dz whose address is a
-    multiple of 16 bytes; 0 covers any dz."""
+def weight_grad_workspace_size(rows, outs, cols, dtype=torch.bfloat16, B=None, lddz=0,
+                               out_dtype=None):
+    """Workspace bytes of weight_grad for dz of `dtype` and dW of `out_dtype` (the same by
+    default).  lddz: the row stride of a dz whose address is a multiple of 16 bytes; 0
+    covers any dz."""
     out = ctypes.c_size_t(0)
     _check(load_library().dash_weight_grad_workspace_size(
-        rows, outs, cols, _DTYPES.get(dtype, -1), lddz, int(B or 0), ctypes.byref(out)),
-        "dash_weight_grad_workspace_size")
+        rows, outs, cols, _DTYPES.get(dtype, -1), _DTYPES.get(out_dtype or dtype, -1), lddz,
+        int(B or 0), ctypes.byref(out)), "dash_weight_grad_workspace_size")
     return out.value
 
 
@@ -885,7 +887,8 @@ def weight_grad(dz, q, scale, cols, fmt="int8", gamma=None, beta=None, B=None, d
     db = torch.empty(outs, dtype=torch.float32, device=dz.device) if bias else None
     pz = dz.data_ptr()
     if ws is None:
-        n = weight_grad_workspace_size(rows, outs, cols, dz.dtype, B, 0 if pz & 15 else lddz)
+        n = weight_grad_workspace_size(rows, outs, cols, dz.dtype, B, 0 if pz & 15 else lddz,
+                                       out.dtype)
         ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dz.device)
     e = lib.weight_grad(pz, _DTYPES.get(dz.dtype, -1), lddz, rows, outs, q.data_ptr(),
                         scale.data_ptr(), f, cols, g, b, wdt, out.data_ptr(), _gdt(out), ldw, B,

@@ -530,6 +530,11 @@ static dash_status part_sum(const float* part, int parts, long long cols, long l
              : DASH_ERR_CUDA;
 }
 
+dash_status launch_part_sum(const float* part, int parts, long long cols, float* out,
+                            cudaStream_t st) {
+  return part_sum(part, parts, cols, cols, out, nullptr, st);
+}
+
 // Slices of the rows: four CTAs per SM, each warp of one with 16 rows or more.
 int col_sum_parts(long long rows, long long cols) {
   const long long tiles = (cols + 255) / 256;

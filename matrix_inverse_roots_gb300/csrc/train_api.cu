@@ -124,11 +124,13 @@ dash_status layer_norm_backward(const void* dy, int64_t lddy, int dt, int64_t ro
 }
 
 dash_status dash_weight_grad_workspace_size(int64_t rows, int64_t outs, int64_t cols, int dt,
-                                            int64_t lddz, int B, size_t* bytes) {
-  if (bytes == nullptr || !valid_weight(rows, outs, cols, B) || !valid_dt(dt) || lddz < 0)
+                                            int odt, int64_t lddz, int B, size_t* bytes) {
+  if (bytes == nullptr || !valid_weight(rows, outs, cols, B) || !valid_dt(dt) || !valid_dt(odt) ||
+      lddz < 0)
     return DASH_ERR_INVALID_ARG;
   WeightGradArgs a = {};
   a.dt = dt;
+  a.odt = odt;
   a.lddz = lddz;
   a.rows = rows;
   a.outs = outs;

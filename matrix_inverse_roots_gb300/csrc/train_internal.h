@@ -106,6 +106,9 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
 int col_sum_parts(long long rows, long long cols);
 dash_status launch_col_sum(const void* m, int dt, long long rows, long long cols, long long ld,
                            float* part, float* out, cudaStream_t st);
+// out[c] = the sum of the rows of part (parts, cols), in order.
+dash_status launch_part_sum(const float* part, int parts, long long cols, float* out,
+                            cudaStream_t st);
 
 inline int dt_bytes(int dt) { return dt == DASH_DT_F32 ? 4 : 2; }
 

@@ -8,28 +8,37 @@
 // as bf16 parts that add up to it (one for bf16, two for fp16, three for fp32).  gamma
 // and beta belong to columns of dW, so they are applied to the sums.
 //
-// Design (persistent, CTA pairs on 256 x 256 tiles of dW, cta_group::2; both operands lie
+// Design (persistent, CTA pairs on 256 x BN tiles of dW, cta_group::2; both operands lie
 // in memory with the token index outermost, so both are MN-major):
 //   warps 0, 3   TMA producers of A: 128 columns of dz per CTA, 64 tokens per slot, each
 //                loading 64 of the columns (one thread starts about 16 KB of tiled copies
 //                per 600 cycles, which the MMAs of a slot nearly take).
-//   warp 2       TMA producer of the codes: 128 columns, 64 tokens (8 KB) per slot.
-//   warps 4, 6-8, 10-15  converters: codes and scales (scales straight from global
-//                memory, one slot ahead) to bf16, into the 128-byte-swizzled layout the MMA
-//                reads.  A slot takes a warp pair about 1500 cycles from its codes to its
-//                hand-over, three times its MMAs, so every ring slot has a pair of its
-//                own.  Measured at 16384 x 8192 x 8192 with int8 codes and five slots:
-//                three pairs 1340 TFLOP/s, four 1570, five 1600.  All but one of them
-//                stay off the scheduler of the MMA warp, whose few instructions would
-//                wait for theirs (hence the idle warps 5 and 9).
+//   warp 2       TMA producer of the codes: BN / 2 columns, 64 tokens per slot.
+//   warps 4-15 (BN = 256) or 4-11 (128)  converters: codes and scales (scales straight from
+//                global memory, one round ahead) to bf16, into the 128-byte-swizzled layout
+//                the MMA reads.  A slot takes its warps about 1500 cycles from its codes
+//                to its hand-over, three times its MMAs, so every ring slot has its own: a
+//                pair for 128 columns, one warp for 64.  Measured at 16384 x 8192 x 8192
+//                with int8 codes, BN = 256 and five slots: three pairs 1340 TFLOP/s, four
+//                1570, five 1600.  Warps 5 and 9 come last: they share a scheduler with
+//                the MMA warp, whose few instructions would wait for theirs.
 //                A converter warp makes its writes visible to the tensor core (proxy
 //                fence) and arrives on the leader's barrier without a cluster-wide fence:
 //                what the arrival orders are writes to this CTA's own shared memory, which
 //                only this SM's tensor core reads, and they are complete before it.  (With
 //                a release at cluster scope each hand-over took about 1400 cycles, more
 //                than twice a slot's MMAs, and the product ran at 850 TFLOP/s.)
-//   warp 1       of the leader issues the MMAs into one of two TMEM accumulators.
-//   warps 16-19  epilogue of the previous tile.
+//   warp 1       of the leader issues the MMAs into one of 512 / BN TMEM accumulators.
+//   warp 9       fills the blocks' padding with zeros, then idles.
+//   the rest     epilogue: 4 warps, or 8 that also reduce (below).
+//
+// Accuracy.  The tensor core adds with truncation: a running sum of M instructions (16
+// tokens of one part each) ends about M / 4 units in the last place of fp32 short.  A
+// 16-bit dW does not show that.  Where dz or dW is fp32, BN is 128 and a sum is cut every
+// SEG instructions or so: eight warps add the pieces to fp32 registers with
+// round-to-nearest, which leaves some 3e-8 SEG, like a plain fp32 product.  It takes half
+// the tile (64 sums per thread), so more shared-memory reads per flop.
+//
 // Tiles that do not fill a whole round of the pairs are split along the tokens; their
 // fp32 partial sums are joined, in order, by a second kernel.
 // Every wait is bounded (see mbar_wait); a time-out sets the device error flag, and the
@@ -51,25 +60,40 @@ int weight_grad_read_clear_error() {
 
 namespace {
 
-constexpr int WT = 256;              // tile of dW per CTA pair (both directions)
-constexpr int WK = 64;               // tokens per slot
-constexpr int W_BOX = WK * 128;      // one box: 64 tokens of 64 bf16 columns or 128 codes
-constexpr int W_GW = 2;              // warps of a converter group, each taking 32 of 64 rows
-constexpr int W_EPI = 4, W_EPI0 = 16;  // epilogue warps
-constexpr int W_THREADS = 32 * (W_EPI0 + W_EPI);
+constexpr int WM = 256;           // rows of dW per tile
+constexpr int WK = 64;            // tokens per slot
+constexpr int W_BOX = WK * 128;   // one box: 64 tokens of 64 bf16 columns or 128 codes
+constexpr int W_THREADS = 640;
+constexpr int SEG = 16;           // instructions per truncated sum, where that is bounded
 
 // A ring slot holds 64 tokens: PARTS tiles of A (128 columns of dz in two boxes), the
-// converted B (128 columns in two boxes) and the codes (one box).
-template <int PARTS>
+// converted B (BN / 2 columns) and the codes.
+template <int BN, int PARTS>
 struct WCfg {
+  static constexpr bool ACC = BN == 128;              // bounded sums
+  static constexpr int BC = BN / 2;                   // columns of B per CTA
   static constexpr int OFF_B = PARTS * 2 * W_BOX;
-  static constexpr int OFF_Q = OFF_B + 2 * W_BOX;
-  static constexpr int SLOT = OFF_Q + W_BOX;
-  static constexpr int NS = (232448 - 1536) / SLOT;  // 5, 4, 3 slots
-  static constexpr int CONV = NS * W_GW;             // converter warps
-  static constexpr int BARS = 4 * NS + 4 + 1;
-  static constexpr int SMEM = NS * SLOT + 1024 + 512;
-  static_assert(NS >= 3 && CONV <= 10 && 8 * BARS + 16 <= 512, "ring, warps, barrier area");
+  static constexpr int OFF_Q = OFF_B + BC / 64 * W_BOX;
+  static constexpr int Q_BYTES = BC * WK;
+  static constexpr int SLOT = OFF_Q + Q_BYTES;
+  static constexpr int GW = BC / 64;                  // converter warps of a slot
+  static constexpr int EPI0 = ACC ? 12 : 16;          // first epilogue warp
+  static constexpr int EPI = 20 - EPI0;
+  static constexpr int CW = BN / (EPI / 4);           // columns of an epilogue warp
+  static constexpr int STAGING = 32 * 17 * 4;         // its 32 rows x 16 columns, padded
+  // gamma and beta of two tiles; staging.
+  static constexpr int EPI_BYTES = 4 * BN * 4 + EPI * STAGING;
+  static constexpr int FIT = (232448 - 1536 - EPI_BYTES) / SLOT;
+  static constexpr int MAXS = ACC ? 7 : 5;
+  static constexpr int NS = FIT < MAXS ? FIT : MAXS;  // slots
+  static constexpr int NACC = 512 / BN;               // TMEM accumulators
+  // Slots per accumulator: all of a unit's, or as many as keep SEG instructions.
+  static constexpr int SEG_SLOTS = ACC ? (SEG / 4 / PARTS > 0 ? SEG / 4 / PARTS : 1) : 1 << 30;
+  static constexpr int BARS = 4 * NS + 2 * NACC + 1;
+  static constexpr int OFF_EPI = NS * SLOT;
+  static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;
+  static_assert(NS >= 3 && 8 * BARS + 16 <= 512 && OFF_BAR % 16 == 0, "ring and barrier area");
 };
 
 struct WParams {
@@ -78,10 +102,12 @@ struct WParams {
   int full;            // tiles computed whole
   int split, kper;     // the others: `split` units of kper slots each
   int units;
+  int bn;
+  int vec_out;         // rows of dW take 16-byte stores
   long long rows, ng;
   const uint8_t* scale;
   const float* db;     // column sums of dz (null without beta)
-  float* partial;      // (units - full) x 256 x 256 sums
+  float* partial;      // (units - full) x 256 x bn sums
   WeightGradArgs a;
 };
 
@@ -149,57 +175,73 @@ __device__ __forceinline__ void store_dt(void* p, int dt, long long i, float v) 
     static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// Scales W consecutive sums of row o from column i on and stores them (W a power of two
-// that divides i; a block's rows hold whole groups of W).  Outside the valid part a block
-// is zero, whatever the sums there (a NaN code meets a zero there).
+// Stores W (4 or 16) consecutive finished values of row o from column i on, of which those
+// below column pc exist.
 template <int W>
-__device__ __forceinline__ void finish_store(const WeightGradArgs& a, const float* db, long long o,
-                                             long long i, float (&v)[W]) {
-  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
-  if (o >= pr || i >= pc) return;
-  const float dbo = (db != nullptr && o < a.outs) ? db[o] : 0.0f;
-#pragma unroll
-  for (int j = 0; j < W; ++j) {
-    if (o < a.outs && i + j < a.cols) {
-      if (a.gamma) v[j] *= load_dt(a.gamma, a.wdt, i + j);
-      if (a.beta) v[j] = fmaf(dbo, load_dt(a.beta, a.wdt, i + j), v[j]);
-    } else {
-      v[j] = 0.0f;
-    }
-  }
+__device__ __forceinline__ void store_row(const WParams& p, long long o, long long i, long long pc,
+                                          const float (&v)[W]) {
+  const WeightGradArgs& a = p.a;
   const long long at = dw_index(a, o, i);
-  if (i + W <= pc) {
-    if (a.odt == DASH_DT_F32) {
-      float* p = static_cast<float*>(a.dw) + at;
-      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+  if (a.odt == DASH_DT_F32) {
+    float* d = static_cast<float*>(a.dw) + at;
 #pragma unroll
-        for (int j = 0; j < W; j += 4)
-          *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        return;
-      }
-    } else {
-      uint16_t* p = static_cast<uint16_t*>(a.dw) + at;
-      if ((reinterpret_cast<uintptr_t>(p) & (W * 2 < 16 ? W * 2 - 1 : 15u)) == 0) {
-        uint32_t r[W / 2];
+    for (int j = 0; j < W; j += 4) {
+      if (p.vec_out && i + j + 4 <= pc) {
+        *reinterpret_cast<float4*>(d + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      } else {
 #pragma unroll
-        for (int j = 0; j < W / 2; ++j)
-          r[j] = a.odt == DASH_DT_BF16 ? pack_bf162(v[2 * j], v[2 * j + 1])
-                                       : pack_half2(v[2 * j], v[2 * j + 1]);
-        if constexpr (W >= 8) {
-#pragma unroll
-          for (int j = 0; j < W / 8; ++j)
-            reinterpret_cast<uint4*>(p)[j] =
-                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-        } else {
-          *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
-        }
-        return;
+        for (int k = 0; k < 4; ++k)
+          if (i + j + k < pc) d[j + k] = v[j + k];
       }
     }
+    return;
   }
+  uint16_t* d = static_cast<uint16_t*>(a.dw) + at;
+  constexpr int V = W < 8 ? W : 8;  // values of one access
 #pragma unroll
-  for (int j = 0; j < W; ++j)
-    if (i + j < pc) store_dt(a.dw, a.odt, at + j, v[j]);
+  for (int j = 0; j < W; j += V) {
+    uint32_t r[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+      r[k] = a.odt == DASH_DT_BF16 ? pack_bf162(v[j + 2 * k], v[j + 2 * k + 1])
+                                   : pack_half2(v[j + 2 * k], v[j + 2 * k + 1]);
+    if (p.vec_out && i + j + V <= pc) {
+      if constexpr (V == 8)
+        *reinterpret_cast<uint4*>(d + j) = make_uint4(r[0], r[1], r[2], r[3]);
+      else
+        *reinterpret_cast<uint2*>(d + j) = make_uint2(r[0], r[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (i + j + k < pc) d[j + k] = static_cast<uint16_t>(r[k / 2] >> (16 * (k & 1)));
+    }
+  }
+}
+
+// Zeros in the blocks' padding beyond the tiles: rows from r0 on, and columns from c0 on of
+// the rows above; thread `id` of `n`.
+__device__ __forceinline__ void pad_zero(const WeightGradArgs& a, long long r0, long long c0,
+                                         long long id, long long n) {
+  if (a.block == 0) return;
+  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+  const long long below = r0 < pr ? (pr - r0) * pc / 4 : 0;
+  const long long w4 = c0 < pc ? (pc - c0) / 4 : 0;
+  const long long total = below + (r0 < pr ? r0 : pr) * w4;
+  for (long long e = id; e < total; e += n) {
+    long long o, i;
+    if (e < below) {
+      o = r0 + e * 4 / pc;
+      i = e * 4 % pc;
+    } else {
+      o = (e - below) / w4;
+      i = c0 + (e - below) % w4 * 4;
+    }
+    const long long at = dw_index(a, o, i);
+    if (a.odt == DASH_DT_F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at) = make_uint2(0u, 0u);
+  }
 }
 
 __device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
@@ -255,28 +297,27 @@ __host__ __device__ constexpr int tmem_col(int j) {
   return (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1);
 }
 
-template <int FMT, int PARTS>
+template <int FMT, int BN, int PARTS>
 __global__ void __launch_bounds__(W_THREADS, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tQ,
                        const __grid_constant__ WParams p) {
-  using C = WCfg<PARTS>;
+  using C = WCfg<BN, PARTS>;
   constexpr int NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw_base + pad;
-  const uint32_t bar0 = sbase + NS * C::SLOT;
+  const uint32_t bar0 = sbase + C::OFF_BAR;
   auto full = [&](int s) { return bar0 + 8u * s; };             // A landed, B converted
   auto empty = [&](int s) { return bar0 + 8u * (NS + s); };     // the MMAs have read both
   auto qfull = [&](int s) { return bar0 + 8u * (2 * NS + s); };
   auto qempty = [&](int s) { return bar0 + 8u * (3 * NS + s); };
   auto tfull = [&](int s) { return bar0 + 8u * (4 * NS + s); };
-  auto tempty = [&](int s) { return bar0 + 8u * (4 * NS + 2 + s); };
+  auto tempty = [&](int s) { return bar0 + 8u * (4 * NS + C::NACC + s); };
   const uint32_t fin_bar = bar0 + 8u * (C::BARS - 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + NS * C::SLOT + 8 * C::BARS);
-  volatile int* abort_flag =
-      reinterpret_cast<volatile int*>(smem + NS * C::SLOT + 8 * C::BARS + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * C::BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 8 * C::BARS + 8);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -290,14 +331,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     for (int s = 0; s < NS; ++s) {
       // Of the leader: its two producers (the bytes of both CTAs) and the slot's
       // converters of both CTAs.
-      mbar_init(full(s), 2 + 2 * W_GW);
+      mbar_init(full(s), 2 + 2 * C::GW);
       mbar_init(empty(s), 1);
       mbar_init(qfull(s), 1);
-      mbar_init(qempty(s), W_GW);
+      mbar_init(qempty(s), C::GW);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::NACC; ++s) {
       mbar_init(tfull(s), 1);
-      mbar_init(tempty(s), 2 * W_EPI);
+      mbar_init(tempty(s), 2 * C::EPI);
     }
     mbar_init(fin_bar, 1);
     *abort_flag = 0;
@@ -312,6 +353,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // Launched while the kernel before it still runs (its parts of dz, its column sums).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0 || warp == 3) {
     if (lane == 0) {
@@ -322,7 +365,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       bool ok = true;
       for (int u = cid; ok && u < p.units; u += ncl) {
         const Unit x = unit_at(u, p);
-        const int o0 = x.mt * WT + static_cast<int>(crank) * 128 + half * 64;
+        const int o0 = x.mt * WM + static_cast<int>(crank) * 128 + half * 64;
         for (int kb = x.k0; kb < x.k1; ++kb) {
           if (!mbar_wait(empty(s), ph ^ 1u, abort_flag)) {
             ok = false;
@@ -346,9 +389,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
           }
         }
       }
-      // After a time-out, one that arms it for both CTAs waits for the copies it counts.
-      // Its barrier also counts the converters, which may have stopped: the wait is
-      // bounded all the same.
+      // After a time-out the thread that arms the barriers waits for the copies they
+      // count.  They also count converters, which may have stopped: bounded all the same.
       if (!ok)
         for (int i = 0; i < NS; ++i)
           if (armed & (1u << i)) mbar_wait_drain(full(i), (armed_par >> i) & 1u);
@@ -361,13 +403,13 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       bool ok = true;
       for (int u = cid; ok && u < p.units; u += ncl) {
         const Unit x = unit_at(u, p);
-        const int i0 = x.nt * WT + static_cast<int>(crank) * 128;
+        const int i0 = x.nt * BN + static_cast<int>(crank) * C::BC;
         for (int kb = x.k0; kb < x.k1; ++kb) {
           if (!mbar_wait(qempty(s), ph ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(qfull(s), W_BOX);
+          mbar_arrive_expect_tx(qfull(s), C::Q_BYTES);
           armed |= 1u << s;
           armed_par = (armed_par & ~(1u << s)) | (ph << s);
           tma_load_3d(sbase + s * C::SLOT + C::OFF_Q, &tQ, qfull(s), i0, kb * WK, 0);
@@ -384,90 +426,110 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // -------------------------------------------------------- MMA issuer
-      // The tensor cores take about 520 cycles for a slot's MMAs of one part; this
-      // thread has to come round in less.  So: one barrier to wait for and one to signal
-      // per slot, the next slot's barrier looked at before this slot's MMAs are issued,
-      // and descriptors that are one addition away from a constant.
-      const uint32_t idesc = make_idesc(1, 1, 1, 256, 256);
+      // The tensor cores take about 520 cycles for a slot's MMAs of one part at BN = 256;
+      // this thread has to come round in less.  So: one barrier to wait for and one to
+      // signal per slot, the next slot's barrier looked at before this slot's MMAs are
+      // issued, and descriptors that are one addition away from a constant.
+      const uint32_t idesc = make_idesc(1, 1, 1, 256, BN);
       const uint64_t d0 = smem_desc(sbase, W_BOX, 1024, LAYOUT_SW128);
       int s = 0, acc = 0;
       uint32_t ph = 0, pacc = 0;
       bool ok = true, ready = false;
       for (int u = cid; ok && u < p.units; u += ncl) {
         const Unit x = unit_at(u, p);
-        if (!mbar_wait(tempty(acc), pacc ^ 1u, abort_flag)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * WT);
-        uint32_t accumulate = 0;
-        for (int kb = x.k0; kb < x.k1; ++kb) {
-          if (!ready && !mbar_wait(full(s), ph, abort_flag)) {
+        for (int kb = x.k0; ok && kb < x.k1;) {
+          if (!mbar_wait(tempty(acc), pacc ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
-          const int sn = s + 1 == NS ? 0 : s + 1;
-          const uint32_t pn = sn == 0 ? ph ^ 1u : ph;
-          ready = mbar_test(full(sn), pn);
           tc_fence_after();
-          const uint64_t da = d0 + static_cast<uint32_t>(s * (C::SLOT >> 4));
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int kk = 0; kk < WK / 16; ++kk) {
-              mma_f16_pair(d, da + ((part * 2 * W_BOX + kk * 16 * 128) >> 4),
-                           da + ((C::OFF_B + kk * 16 * 128) >> 4), idesc, accumulate);
-              accumulate = 1;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+          uint32_t accumulate = 0;
+          const int end = C::ACC && x.k1 - kb > C::SEG_SLOTS ? kb + C::SEG_SLOTS : x.k1;
+          for (; kb < end; ++kb) {
+            if (!ready && !mbar_wait(full(s), ph, abort_flag)) {
+              ok = false;
+              break;
             }
-          mma_commit_pair_mc(empty(s), kMask);
-          s = sn;
-          ph = pn;
+            const int sn = s + 1 == NS ? 0 : s + 1;
+            const uint32_t pn = sn == 0 ? ph ^ 1u : ph;
+            ready = mbar_test(full(sn), pn);
+            tc_fence_after();
+            const uint64_t da = d0 + static_cast<uint32_t>(s * (C::SLOT >> 4));
+            // The small parts first, while the sum is small.
+#pragma unroll
+            for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+              for (int kk = 0; kk < WK / 16; ++kk) {
+                mma_f16_pair(d, da + ((part * 2 * W_BOX + kk * 16 * 128) >> 4),
+                             da + ((C::OFF_B + kk * 16 * 128) >> 4), idesc, accumulate);
+                accumulate = 1;
+              }
+            mma_commit_pair_mc(empty(s), kMask);
+            s = sn;
+            ph = pn;
+          }
+          if (!ok) break;
+          mma_commit_pair_mc(tfull(acc), kMask);
+          if (++acc == C::NACC) {
+            acc = 0;
+            pacc ^= 1u;
+          }
         }
-        if (!ok) break;
-        mma_commit_pair_mc(tfull(acc), kMask);
-        acc ^= 1;
-        if (acc == 0) pacc ^= 1u;
       }
       // Every MMA issued above must be complete before TMEM is released.
       mma_commit_pair(fin_bar);
       mbar_wait_drain(fin_bar, 0);
     }
-  } else if (warp < W_EPI0) {
+  } else if (warp < C::EPI0) {
     // ---------------------------------------------------------- converters
-    // Converter number 0 .. 9 of the warp (5 and 9 have none).  Group s takes ring slot s,
-    // every time: what it waits on there it has followed phase by phase, so a parity is
-    // never ambiguous.  A warp takes 32 of a slot's rows, eight lanes a row of 128 columns,
-    // four rows at a time.
-    const int conv = (warp == 5 || warp == 9) ? -1 : warp - 4 - (warp > 5) - (warp > 9);
-    const int s = conv / W_GW;
-    uint32_t par = 0;
-    // The lanes of the upper 64 columns (box 1) take the neighbouring row, whose swizzle
-    // differs in the lowest bit: the eight lanes of an access then hit all banks once.
-    const int c16 = lane & 7, odd = c16 >> 2;
-    const int rl = (lane >> 3) ^ odd;  // row, of the four
-    const int t0 = (conv % W_GW) * 32 + rl;
-    const int w = (c16 & 3) * 2;       // its 16-byte words are w and w + 1 of the box's row
-    const int qoff = C::OFF_Q + t0 * 128 + c16 * 16;
-    const int boff = C::OFF_B + odd * W_BOX + t0 * 128;
+    // Numbers 0, 1, ... of the warps, 5 and 9 last.  Slot s is converted by warps GW s ...
+    // every time: what they wait on there they have followed phase by phase, so a parity
+    // is never ambiguous.  A warp takes 32 rows of 128 columns, eight lanes a row, or 64
+    // rows of 64, four lanes a row; 16 columns per lane, eight passes.
+    constexpr int LR = C::BC / 16;  // lanes of a row
+    constexpr int RP = 32 / LR;     // rows of a pass
+    const int conv = warp == 5 ? C::EPI0 - 6
+                     : warp == 9 ? C::EPI0 - 5
+                                 : warp - 4 - (warp > 5) - (warp > 9);
+    const int s = conv / C::GW;
+    const int rbase = (conv % C::GW) * 32;
+    const int c16 = lane % LR, odd = c16 >> 2;
+    // The eight lanes of an access hit all banks once: their two groups of four lie in
+    // neighbouring rows, whose swizzles differ in the lowest bit.  (With two boxes the
+    // lanes of the upper one take the neighbouring row for that.)
+    const int rl = (lane / LR) ^ odd;
+    const int t0 = rbase + rl;
+    const int w = (c16 & 3) * 2;  // its 16-byte words are w and w + 1 of the box's row
     uint8_t* const slot = smem + s * C::SLOT;
+    const int qoff = C::OFF_Q + t0 * C::BC + c16 * 16;
+    const int boff = C::OFF_B + odd * W_BOX + t0 * 128;
     const uint32_t sel = 0x4040u | ((c16 >> 1) * 0x0101u);  // the group's byte to bytes 0, 2
-    int ahead = s;  // slots from the unit's first to the group's next
-    const bool words = (p.ng & 3) == 0 && (reinterpret_cast<uintptr_t>(p.scale) & 3u) == 0;
-    bool ok = conv >= 0 && conv < C::CONV;
+    uint32_t par = 0;
+    int ahead = s;  // slots from the unit's first to the next one to convert
+    constexpr int NG = C::BC / Q8_GROUP;  // scales of a row: 4 or 2
+    const bool words = p.ng % NG == 0 && (reinterpret_cast<uintptr_t>(p.scale) & (NG - 1)) == 0;
+    bool ok = conv < NS * C::GW;
     for (int u = cid; ok && u < p.units; u += ncl) {
       const Unit x = unit_at(u, p);
-      const int g0 = x.nt * (WT / Q8_GROUP) + static_cast<int>(crank) * 4;
-      // The four scale bytes of row 32 (conv % W_GW) + lane of slot kb; 0 (a scale of 0)
-      // outside.
+      const int g0 = x.nt * (BN / Q8_GROUP) + static_cast<int>(crank) * NG;
+      // The scale bytes of a row of slot kb (4), or of rows `lane` and 32 + lane (2 each);
+      // 0 (a scale of 0) outside.
       auto scales = [&](int kb) -> uint32_t {
-        const long long r = static_cast<long long>(kb) * WK + (conv % W_GW) * 32 + lane;
         uint32_t v = 0;
-        if (kb < x.k1 && r < p.rows && g0 < p.ng) {
+        if (kb >= x.k1 || g0 >= p.ng) return v;
+#pragma unroll
+        for (int h = 0; h < 4 / NG; ++h) {
+          const long long r = static_cast<long long>(kb) * WK + rbase + h * 32 + lane;
+          if (r >= p.rows) continue;
           const uint8_t* sp = p.scale + r * p.ng + g0;
           if (words) {
-            v = *reinterpret_cast<const uint32_t*>(sp);
+            v |= NG == 4 ? *reinterpret_cast<const uint32_t*>(sp)
+                         : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp)) << (16 * h);
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (g0 + j < p.ng) v |= static_cast<uint32_t>(sp[j]) << (8 * j);
+            for (int j = 0; j < NG; ++j)
+              if (g0 + j < p.ng) v |= static_cast<uint32_t>(sp[j]) << (16 * h + 8 * j);
           }
         }
         return v;
@@ -483,66 +545,189 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         uint4 q[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          q[j] = *reinterpret_cast<const uint4*>(slot + qoff + j * 4 * 128);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qempty(s));
+          q[j] = *reinterpret_cast<const uint4*>(slot + qoff + j * RP * C::BC);
         uint8_t* dst = slot + boff;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t four = __shfl_sync(0xffffffffu, sc, j * 4 + rl);
+          // Row rl + j RP of the warp's rows: its scales are lane (row % 32)'s.
+          uint32_t four = __shfl_sync(0xffffffffu, sc, (j * RP + rl) & 31);
+          if (NG == 2 && j * RP >= 32) four >>= 16;
           uint4 lo, hi;
           convert16<FMT>(q[j], scale_bf2(__byte_perm(four, 0u, sel)), lo, hi);
-          const int sw = (t0 + j * 4) & 7;
-          uint8_t* r0 = dst + j * 4 * 128;
+          const int sw = (t0 + j * RP) & 7;
+          uint8_t* r0 = dst + j * RP * 128;
           *reinterpret_cast<uint4*>(r0 + ((w ^ sw) << 4)) = lo;
           *reinterpret_cast<uint4*>(r0 + (((w + 1) ^ sw) << 4)) = hi;
         }
+        // The codes are given back after the stores that depend on them: an arrival right
+        // after the loads does not keep the assembler from sinking a load below it (one
+        // did sink, and now and then took the codes of the slot's next use).
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(full(s), 0));
+        if (lane == 0) {
+          mbar_arrive(qempty(s));
+          mbar_arrive_remote(mapa_shared(full(s), 0));
+        }
         sc = next;
         par ^= 1u;
       }
       ahead = kb - x.k1;
     }
+    if (warp == 9)
+      pad_zero(p.a, static_cast<long long>(p.tiles_m) * WM, static_cast<long long>(p.tiles_n) * BN,
+               static_cast<long long>(blockIdx.x) * 32 + lane,
+               static_cast<long long>(gridDim.x) * 32);
   } else {
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3;  // TMEM lane quarter
-    int acc = 0;
+    const int q = warp & 3;                             // TMEM lane quarter
+    const int col0 = ((warp - C::EPI0) >> 2) * C::CW;   // first column of this warp
+    const int et = threadIdx.x - 32 * C::EPI0;
+    float* gb = reinterpret_cast<float*>(smem + C::OFF_EPI);  // [parity][gamma, beta][BN]
+    float* staging = reinterpret_cast<float*>(smem + C::OFF_EPI + 4 * BN * 4 +
+                                              (warp - C::EPI0) * C::STAGING);
+    const WeightGradArgs& a = p.a;
+    const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+    int acc = 0, gp = 0;
     uint32_t pacc = 0;
-    for (int u = cid; u < p.units; u += ncl) {
+    bool ok = true;
+    for (int u = cid; ok && u < p.units; u += ncl, gp ^= 1) {
       const Unit x = unit_at(u, p);
-      if (!mbar_wait(tfull(acc), pacc, abort_flag)) break;
-      tc_fence_after();
+      // gamma and beta of the tile's columns, while its product runs.  (A buffer is
+      // rewritten two tiles later, past the barrier of the tile between.)
+      float* gm = gb + gp * 2 * BN;
+      for (int j = et; j < BN; j += 32 * C::EPI) {
+        const long long i = static_cast<long long>(x.nt) * BN + j;
+        gm[j] = a.gamma && i < a.cols ? load_dt(a.gamma, a.wdt, i) : 1.0f;
+        gm[BN + j] = a.beta && i < a.cols ? load_dt(a.beta, a.wdt, i) : 0.0f;
+      }
       const int row = static_cast<int>(crank) * 128 + q * 32 + lane;  // in the tile
-      const uint32_t taddr =
-          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * WT);
-#pragma unroll 1
-      for (int cc = 0; cc < WT / 16; ++cc) {
-        uint32_t r[16];
-        tmem_ld16(taddr + cc * 16, r);
-        tmem_wait_ld(r);
-        if (cc + 1 == WT / 16) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
-        }
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[tmem_col(j)]);
+      const long long o = static_cast<long long>(x.mt) * WM + row;
+      const float dbo = p.db != nullptr && o < a.outs ? p.db[o] : 0.0f;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * C::EPI) : "memory");
+      // Whether every element of the tile is one of dW.
+      const bool inside = static_cast<long long>(x.mt + 1) * WM <= a.outs &&
+                          static_cast<long long>(x.nt + 1) * BN <= a.cols;
+      // Finishes 16 sums of this lane's row from the tile's column c on.
+      auto finish = [&](int c, float (&v)[16]) {
         if (x.part >= 0) {
           float4* d = reinterpret_cast<float4*>(
-              p.partial + (static_cast<long long>(x.part) * WT + row) * WT + cc * 16);
+              p.partial + (static_cast<long long>(x.part) * WM + row) * BN + c);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        } else {
-          finish_store<16>(p.a, p.db, static_cast<long long>(x.mt) * WT + row,
-                           static_cast<long long>(x.nt) * WT + cc * 16, v);
+          return;
+        }
+        const long long i = static_cast<long long>(x.nt) * BN + c;
+        if (i >= pc) return;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 g = *reinterpret_cast<const float4*>(gm + c + j);
+          v[j] *= g.x;
+          v[j + 1] *= g.y;
+          v[j + 2] *= g.z;
+          v[j + 3] *= g.w;
+        }
+        if (a.beta) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(gm + BN + c + j);
+            v[j] = fmaf(dbo, b.x, v[j]);
+            v[j + 1] = fmaf(dbo, b.y, v[j + 1]);
+            v[j + 2] = fmaf(dbo, b.z, v[j + 2]);
+            v[j + 3] = fmaf(dbo, b.w, v[j + 3]);
+          }
+        }
+        if (!inside) {
+          // Outside dW a block is zero, whatever the sums there (a NaN code meets a zero).
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (o >= a.outs || i + j >= a.cols) v[j] = 0.0f;
+        }
+        if (p.vec_out) {
+          if (o < pr) store_row<16>(p, o, i, pc, v);
+          return;
+        }
+        // Rows that no vector store fits: through shared memory, so that a store's lanes
+        // hold neighbouring columns.
+#pragma unroll
+        for (int j = 0; j < 16; ++j) staging[lane * 17 + j] = v[j];
+        __syncwarp();
+        const int cl = lane & 15;
+        const long long o0 = o - lane;
+#pragma unroll
+        for (int r = lane >> 4; r < 32; r += 2)
+          if (o0 + r < pr && i + cl < pc)
+            store_dt(a.dw, a.odt, dw_index(a, o0 + r, i + cl), staging[r * 17 + cl]);
+        __syncwarp();
+      };
+      if constexpr (C::ACC) {
+        uint64_t sum[C::CW / 2];
+#pragma unroll
+        for (int j = 0; j < C::CW / 2; ++j) sum[j] = 0ull;
+        for (int kb = x.k0; kb < x.k1; kb += C::SEG_SLOTS) {
+          if (!mbar_wait(tfull(acc), pacc, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                 static_cast<uint32_t>(acc * BN + col0);
+#pragma unroll
+          for (int c = 0; c < C::CW / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld16(taddr + c * 16, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              f32x2_add_rn(sum[c * 8 + j], f32x2_pack(r[2 * j], r[2 * j + 1]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+          if (++acc == C::NACC) {
+            acc = 0;
+            pacc ^= 1u;
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < C::CW / 16; ++c) {
+          uint32_t r[16];
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f32x2_unpack(sum[c * 8 + j], r[2 * j], r[2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[tmem_col(j)]);
+          finish(col0 + c * 16, v);
+        }
+      } else {
+        if (!mbar_wait(tfull(acc), pacc, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>(acc * BN + col0);
+#pragma unroll 1
+        for (int c = 0; c < C::CW / 16; ++c) {
+          uint32_t r[16];
+          tmem_ld16(taddr + c * 16, r);
+          tmem_wait_ld(r);
+          if (c + 1 == C::CW / 16) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+          }
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[tmem_col(j)]);
+          finish(col0 + c * 16, v);
+        }
+        if (++acc == C::NACC) {
+          acc = 0;
+          pacc ^= 1u;
         }
       }
-      acc ^= 1;
-      if (acc == 0) pacc ^= 1u;
     }
   }
 
@@ -557,77 +742,117 @@ __global__ void __launch_bounds__(W_THREADS, 1)
   }
 }
 
-// Joins the partial sums of the tiles split along the tokens (none at all for split 0, a
-// gradient over no tokens).  A warp per 128 columns of a tile's row.
+// Joins the partial sums of the tiles split along the tokens, four columns per thread; with
+// split 0 (a gradient over no tokens) there are none, and the padding is filled here too.
 __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_constant__ WParams p,
                                                                int first, int ntiles) {
-  const long long total = static_cast<long long>(ntiles) * WT * (WT / 4);
-  for (long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; e < total;
-       e += static_cast<long long>(gridDim.x) * 256) {
-    const int c4 = static_cast<int>(e % (WT / 4));
-    const long long rr = e / (WT / 4);
-    const int row = static_cast<int>(rr % WT);
-    const int t = static_cast<int>(rr / WT);
+  const WeightGradArgs& a = p.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+  const int w4 = p.bn / 4;
+  const long long total = static_cast<long long>(ntiles) * WM * w4;
+  const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long n = static_cast<long long>(gridDim.x) * 256;
+  for (long long e = id; e < total; e += n) {
+    const int c4 = static_cast<int>(e % w4);
+    const long long rr = e / w4;
+    const int row = static_cast<int>(rr % WM);
+    const int t = static_cast<int>(rr / WM);
     int mt, nt;
     tile_at(first + t, p.tiles_m, p.tiles_n, mt, nt);
+    const long long o = static_cast<long long>(mt) * WM + row;
+    const long long i = static_cast<long long>(nt) * p.bn + c4 * 4;
+    if (o >= pr || i >= pc) continue;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
     for (int s = 0; s < p.split; ++s) {
       const float4 f = *reinterpret_cast<const float4*>(
-          p.partial + ((static_cast<long long>(t) * p.split + s) * WT + row) * WT + c4 * 4);
+          p.partial + ((static_cast<long long>(t) * p.split + s) * WM + row) * p.bn + c4 * 4);
       v[0] += f.x;
       v[1] += f.y;
       v[2] += f.z;
       v[3] += f.w;
     }
-    finish_store<4>(p.a, p.db, static_cast<long long>(mt) * WT + row,
-                    static_cast<long long>(nt) * WT + c4 * 4, v);
-  }
-}
-
-// Zeros in the blocks' padding that no tile reaches: rows from r0 on, and columns from c0.
-__global__ void __launch_bounds__(256)
-    weight_grad_pad_kernel(const WeightGradArgs a, long long r0, long long c0) {
-  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
-  for (long long o = blockIdx.y; o < pr; o += gridDim.y) {
-    const long long from = o < r0 ? c0 : 0;
-    for (long long i = from + (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4; i < pc;
-         i += static_cast<long long>(gridDim.x) * 1024) {
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const long long at = dw_index(a, o, i);
-      if (a.odt == DASH_DT_F32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at) =
-            make_float4(v[0], v[1], v[2], v[3]);
-      else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at) = make_uint2(0u, 0u);
-    }
-  }
-}
-
-// dz as bf16 parts that add up to it, (parts, rows, ldp).  Every part but the last keeps
-// the upper bits (truncated, so that no part overflows); what is left is exact.
-template <typename T, int PARTS>
-__global__ void __launch_bounds__(256)
-    split_kernel(const T* dz, long long rows, long long outs, long long ld, long long ldp,
-                 uint16_t* out) {
-  for (long long r = blockIdx.y; r < rows; r += gridDim.y)
-    for (long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; c < outs;
-         c += static_cast<long long>(gridDim.x) * 256) {
-      float v = Elem<T>::to(dz[r * ld + c]);
+    const float dbo = p.db != nullptr && o < a.outs ? p.db[o] : 0.0f;
 #pragma unroll
-      for (int k = 0; k < PARTS; ++k) {
-        const uint32_t b = __float_as_uint(v) & 0xffff0000u;
-        uint32_t h = b >> 16;
-        // Non-finite: the first part carries it (a NaN keeps a mantissa bit), the others
-        // are zero.
-        if ((b & 0x7f800000u) == 0x7f800000u) {
-          if (v != v) h = 0x7fc0u;
-          v = 0.0f;
-        } else {
-          v -= __uint_as_float(b);
-        }
-        out[(k * rows + r) * ldp + c] = static_cast<uint16_t>(h);
+    for (int j = 0; j < 4; ++j) {
+      if (o < a.outs && i + j < a.cols) {
+        if (a.gamma) v[j] *= load_dt(a.gamma, a.wdt, i + j);
+        if (a.beta) v[j] = fmaf(dbo, load_dt(a.beta, a.wdt, i + j), v[j]);
+      } else {
+        v[j] = 0.0f;
       }
     }
+    store_row<4>(p, o, i, pc, v);
+  }
+  if (p.split == 0)
+    pad_zero(a, static_cast<long long>(p.tiles_m) * WM, static_cast<long long>(p.tiles_n) * p.bn,
+             id, n);
+}
+
+// dz as bf16 parts that add up to it, (parts, rows, ldp), and, where `sums` is given, its
+// column sums over the rows of slice blockIdx.y: the same reads serve both.  Every part but
+// the last keeps the upper bits (truncated, so that no part overflows); what is left is
+// exact.  256 columns per CTA, eight per lane, rows dealt to the warps.
+template <typename T, int PARTS, bool VEC>
+__global__ void __launch_bounds__(256)
+    split_kernel(const T* dz, long long rows, long long outs, long long ld, long long ldp,
+                 long long slice, uint16_t* out, float* sums) {
+  __shared__ float sb[8][256];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long c = static_cast<long long>(blockIdx.x) * 256 + lane * 8;
+  const int n = static_cast<int>(outs - c < 8 ? outs - c : 8);
+  const long long r0 = blockIdx.y * slice;
+  const long long r1 = r0 + slice < rows ? r0 + slice : rows;
+  F2 s[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
+#pragma unroll 2
+  for (long long r = r0 + w; r < r1; r += 8) {
+    F2 v[4];
+    load8<T, VEC>(dz + r * ld + c, n, v);
+    uint32_t word[PARTS][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s[k] = s[k] + v[k];
+      float f[2];
+      f2_get(v[k], f[0], f[1]);
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        uint32_t h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t b = __float_as_uint(f[e]) & 0xffff0000u;
+          h[e] = b >> 16;
+          // Non-finite: the first part carries it (a NaN keeps a mantissa bit), the
+          // others are zero.
+          if ((b & 0x7f800000u) == 0x7f800000u) {
+            if (f[e] != f[e]) h[e] = 0x7fc0u;
+            f[e] = 0.0f;
+          } else {
+            f[e] -= __uint_as_float(b);
+          }
+        }
+        word[q][k] = h[0] | (h[1] << 16);
+      }
+    }
+    // ldp is a multiple of 8 that holds every column: whole words past the last column
+    // are the row's padding.
+    if (n > 0)
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+        *reinterpret_cast<uint4*>(out + (q * rows + r) * ldp + c) =
+            make_uint4(word[q][0], word[q][1], word[q][2], word[q][3]);
+  }
+  if (sums == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f2_get(s[k], sb[w][lane * 8 + 2 * k], sb[w][lane * 8 + 2 * k + 1]);
+  __syncthreads();
+  const long long col = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (col < outs) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += sb[i][threadIdx.x];
+    sums[static_cast<long long>(blockIdx.y) * outs + col] = t;
+  }
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -667,17 +892,21 @@ bool make_map(CUtensorMap* m, const void* base, bool bytes, uint64_t inner, uint
 
 typedef void (*WKernel)(CUtensorMap, CUtensorMap, WParams);
 
-WKernel kernel_of(int fmt, int parts) {
-  if (fmt == DASH_Q8_INT8)
-    return parts == 1   ? weight_grad_kernel<DASH_Q8_INT8, 1>
-           : parts == 2 ? weight_grad_kernel<DASH_Q8_INT8, 2>
-                        : weight_grad_kernel<DASH_Q8_INT8, 3>;
-  return parts == 1   ? weight_grad_kernel<DASH_Q8_E4M3, 1>
-         : parts == 2 ? weight_grad_kernel<DASH_Q8_E4M3, 2>
-                      : weight_grad_kernel<DASH_Q8_E4M3, 3>;
+struct WInst {
+  WKernel k;
+  int smem;
+};
+template <int FMT>
+WInst inst_f(int bn, int parts) {
+  if (bn == 256)
+    return parts == 1 ? WInst{weight_grad_kernel<FMT, 256, 1>, WCfg<256, 1>::SMEM}
+                      : WInst{weight_grad_kernel<FMT, 256, 2>, WCfg<256, 2>::SMEM};
+  return parts == 1   ? WInst{weight_grad_kernel<FMT, 128, 1>, WCfg<128, 1>::SMEM}
+         : parts == 2 ? WInst{weight_grad_kernel<FMT, 128, 2>, WCfg<128, 2>::SMEM}
+                      : WInst{weight_grad_kernel<FMT, 128, 3>, WCfg<128, 3>::SMEM};
 }
-int smem_of(int parts) {
-  return parts == 1 ? WCfg<1>::SMEM : (parts == 2 ? WCfg<2>::SMEM : WCfg<3>::SMEM);
+WInst inst_of(int fmt, int bn, int parts) {
+  return fmt == DASH_Q8_INT8 ? inst_f<DASH_Q8_INT8>(bn, parts) : inst_f<DASH_Q8_E4M3>(bn, parts);
 }
 
 // CTA pairs that can be resident at once, per device; 0 on error.
@@ -696,20 +925,20 @@ int resident_pairs() {
     cfg.blockDim = dim3(W_THREADS, 1, 1);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 1 << 30;
+    int n = device_sm_count() / 2;
     for (int fmt : {DASH_Q8_INT8, DASH_Q8_E4M3})
-      for (int parts = 1; parts <= 3; ++parts) {
-        const void* k = reinterpret_cast<const void*>(kernel_of(fmt, parts));
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(parts)) !=
+      for (int i = 0; i < 5; ++i) {
+        const WInst w = inst_of(fmt, i < 2 ? 256 : 128, i < 2 ? i + 1 : i - 1);
+        const void* k = reinterpret_cast<const void*>(w.k);
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, w.smem) !=
             cudaSuccess)
           return 0;
-        cfg.dynamicSmemBytes = smem_of(parts);
+        cfg.dynamicSmemBytes = w.smem;
         int m = 0;
         if (cudaOccupancyMaxActiveClusters(&m, k, &cfg) != cudaSuccess) return 0;
         n = m < n ? m : n;
       }
-    const int sms = device_sm_count() / 2;
-    cache[dev] = n < sms ? n : sms;
+    cache[dev] = n;
   }
   return cache[dev];
 }
@@ -720,30 +949,32 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // there are, the rest split along the tokens.  A split into S costs ceil(tail S / P)
 // rounds of nkb / S slots; its partial tiles are written and read back once (about 0.1 us
 // each when every pair does so) and a second launch joins them.  In units of one slot's
-// 4 MMAs, about 0.3 us.
+// MMAs of 256 x 256, about 0.4 us.
 struct Plan {
-  int tiles_m, tiles_n, nkb, parts, full, split, kper, units;
+  int bn, tiles_m, tiles_n, nkb, parts, full, split, kper, units;
 };
 
 Plan make_plan(const WeightGradArgs& a, int pairs) {
   Plan p;
-  p.tiles_m = static_cast<int>((a.outs + WT - 1) / WT);
-  p.tiles_n = static_cast<int>((a.cols + WT - 1) / WT);
-  p.nkb = static_cast<int>((a.rows + WK - 1) / WK);
   p.parts = a.dt == DASH_DT_F32 ? 3 : (a.dt == DASH_DT_F16 ? 2 : 1);
+  p.bn = a.dt == DASH_DT_F32 || a.odt == DASH_DT_F32 ? 128 : 256;
+  p.tiles_m = static_cast<int>((a.outs + WM - 1) / WM);
+  p.tiles_n = static_cast<int>((a.cols + p.bn - 1) / p.bn);
+  p.nkb = static_cast<int>((a.rows + WK - 1) / WK);
   const int tiles = p.tiles_m * p.tiles_n;
   const int tail = tiles % pairs;
+  const double slot = p.parts * p.bn / 256.0;
   p.full = tiles;
   p.split = 1;
   p.kper = p.nkb;
-  double best = tail ? static_cast<double>(p.nkb) * p.parts : 0.0;
+  double best = tail ? p.nkb * slot : 0.0;
   const int most = p.nkb / 4 < 64 ? p.nkb / 4 : 64;
   for (int s = 2; tail && s <= most; ++s) {
     const int kper = (p.nkb + s - 1) / s;
     const int se = (p.nkb + kper - 1) / kper;
     if (se < 2) continue;
-    const double cost = static_cast<double>((tail * se + pairs - 1) / pairs) * kper * p.parts +
-                        12.0 + 0.3 * tail * se;
+    const double cost = static_cast<double>((tail * se + pairs - 1) / pairs) * kper * slot + 10.0 +
+                        0.25 * tail * se * p.bn / 256.0;
     if (cost < best) {
       best = cost;
       p.full = tiles - tail;
@@ -764,22 +995,26 @@ bool dz_direct(const WeightGradArgs& a) {
 long long part_ld(const WeightGradArgs& a) { return (a.outs + 7) / 8 * 8; }
 
 template <typename T, int PARTS>
-cudaError_t run_split(const WeightGradArgs& a, uint16_t* out, cudaStream_t st) {
-  const long long gx = (a.outs + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(gx < 64 ? gx : 64),
-                  static_cast<unsigned>(a.rows < 65535 ? a.rows : 65535));
-  split_kernel<T, PARTS><<<grid, 256, 0, st>>>(static_cast<const T*>(a.dz), a.rows, a.outs,
-                                               a.lddz, part_ld(a), out);
+cudaError_t run_split(const WeightGradArgs& a, uint16_t* out, float* sums, cudaStream_t st) {
+  const int parts = col_sum_parts(a.rows, a.outs);
+  const long long slice = (a.rows + parts - 1) / parts;
+  const dim3 grid(static_cast<unsigned>((a.outs + 255) / 256), static_cast<unsigned>(parts));
+  const T* dz = static_cast<const T*>(a.dz);
+  const bool vec = a.outs % 8 == 0 && (reinterpret_cast<uintptr_t>(dz) & 15u) == 0 &&
+                   a.lddz * sizeof(T) % 16 == 0;
+  if (vec)
+    split_kernel<T, PARTS, true>
+        <<<grid, 256, 0, st>>>(dz, a.rows, a.outs, a.lddz, part_ld(a), slice, out, sums);
+  else
+    split_kernel<T, PARTS, false>
+        <<<grid, 256, 0, st>>>(dz, a.rows, a.outs, a.lddz, part_ld(a), slice, out, sums);
   return cudaGetLastError();
 }
 
-}  // namespace
-
 // Workspace: db (when only beta needs it), the column sums' partials, dz's parts, the
-// partial tiles.  Without a device (sizes asked for on the host alone) the most partial
-// tiles any number of pairs can need.
-static size_t carve(const WeightGradArgs& a, const Plan& p, size_t& o_part, size_t& o_dz,
-                    size_t& o_tiles) {
+// partial tiles.
+size_t carve(const WeightGradArgs& a, const Plan& p, size_t& o_part, size_t& o_dz,
+             size_t& o_tiles) {
   size_t n = round256(static_cast<size_t>(a.outs) * 4);
   o_part = n;
   n += round256(static_cast<size_t>(a.outs) * 4 * col_sum_parts(a.rows, a.outs));
@@ -787,11 +1022,25 @@ static size_t carve(const WeightGradArgs& a, const Plan& p, size_t& o_part, size
   if (!dz_direct(a))
     n += round256(static_cast<size_t>(p.parts) * a.rows * part_ld(a) * 2);
   o_tiles = n;
-  n += static_cast<size_t>(p.units - p.full) * WT * WT * 4;
+  n += static_cast<size_t>(p.units - p.full) * WM * p.bn * 4;
   return n;
 }
 
+// Launch attributes: clusters of two, started while the kernel before still runs.
+int attrs(cudaLaunchAttribute (&at)[2], bool cluster) {
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  return cluster ? 2 : 1;
+}
+
+}  // namespace
+
 size_t weight_grad_ws(const WeightGradArgs& a) {
+  // Without a device (sizes asked for on the host alone): a GB300's 76 pairs.
   const int pairs = resident_pairs();
   size_t x, y, z;
   return carve(a, make_plan(a, pairs > 0 ? pairs : 76), x, y, z);
@@ -804,15 +1053,30 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
   size_t o_part, o_dz, o_tiles;
   carve(a, plan, o_part, o_dz, o_tiles);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  float* db = a.db;
-  if (a.db || a.beta) {
-    if (!db) db = reinterpret_cast<float*>(w);
-    const dash_status s = launch_col_sum(a.dz, a.dt, a.rows, a.outs, a.lddz,
-                                         reinterpret_cast<float*>(w + o_part), db, st);
+  float* db = a.db ? a.db : reinterpret_cast<float*>(w);
+  float* sums = a.db || a.beta ? reinterpret_cast<float*>(w + o_part) : nullptr;
+  const bool direct = dz_direct(a) || a.rows == 0;
+  cudaError_t err = cudaSuccess;
+  if (!direct) {
+    uint16_t* out = reinterpret_cast<uint16_t*>(w + o_dz);
+    const int rec = trace_begin(st);
+    if (a.dt == DASH_DT_F32)
+      err = run_split<float, 3>(a, out, sums, st);
+    else if (a.dt == DASH_DT_F16)
+      err = run_split<__half, 2>(a, out, sums, st);
+    else
+      err = run_split<__nv_bfloat16, 1>(a, out, sums, st);
+    trace_end(rec, st, DASH_TRACE_REDUCE, 0.0,
+              static_cast<double>(a.rows) * a.outs * (dt_bytes(a.dt) + 2 * plan.parts));
+    if (err != cudaSuccess) return DASH_ERR_CUDA;
+  }
+  if (sums) {
+    const dash_status s = direct ? launch_col_sum(a.dz, a.dt, a.rows, a.outs, a.lddz, sums, db, st)
+                                 : launch_part_sum(sums, col_sum_parts(a.rows, a.outs), a.outs,
+                                                   db, st);
     if (s != DASH_OK) return s;
   }
   const int rec = trace_begin(st);
-  cudaError_t err = cudaSuccess;
   WParams p = {};
   p.nkb = plan.nkb;
   p.tiles_m = plan.tiles_m;
@@ -821,49 +1085,37 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
   p.split = plan.split;
   p.kper = plan.kper;
   p.units = plan.units;
+  p.bn = plan.bn;
+  const long long orow = a.block ? a.block : a.ldw;
+  p.vec_out = (reinterpret_cast<uintptr_t>(a.dw) & 15u) == 0 && orow * dt_bytes(a.odt) % 16 == 0;
   p.rows = a.rows;
   p.ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP;
   p.scale = a.scale;
   p.db = a.beta ? db : nullptr;
   p.partial = reinterpret_cast<float*>(w + o_tiles);
   p.a = a;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  cfg.stream = st;
+  cfg.attrs = at;
   if (a.rows > 0) {
-    const void* dz = a.dz;
-    uint64_t row_bytes = static_cast<uint64_t>(a.lddz) * 2, plane_bytes = row_bytes * a.rows;
-    if (!dz_direct(a)) {
-      uint16_t* out = reinterpret_cast<uint16_t*>(w + o_dz);
-      if (a.dt == DASH_DT_F32)
-        err = run_split<float, 3>(a, out, st);
-      else if (a.dt == DASH_DT_F16)
-        err = run_split<__half, 2>(a, out, st);
-      else
-        err = run_split<__nv_bfloat16, 1>(a, out, st);
-      dz = out;
-      row_bytes = static_cast<uint64_t>(part_ld(a)) * 2;
-      plane_bytes = row_bytes * a.rows;
-    }
+    const void* dz = direct ? a.dz : w + o_dz;
+    const uint64_t row_bytes = static_cast<uint64_t>(direct ? a.lddz : part_ld(a)) * 2;
     CUtensorMap tA, tQ;
-    if (err != cudaSuccess ||
-        !make_map(&tA, dz, false, a.outs, a.rows, plan.parts, row_bytes, plane_bytes, 64, WK,
-                  true) ||
+    const int bc = plan.bn / 2;
+    if (!make_map(&tA, dz, false, a.outs, a.rows, plan.parts, row_bytes, row_bytes * a.rows, 64,
+                  WK, true) ||
         !make_map(&tQ, a.q, true, p.ng * Q8_GROUP, a.rows, 1, p.ng * Q8_GROUP,
-                  static_cast<uint64_t>(p.ng) * Q8_GROUP * a.rows, 128, WK, false)) {
+                  static_cast<uint64_t>(p.ng) * Q8_GROUP * a.rows, bc, WK, false)) {
       trace_end(rec, st, DASH_TRACE_GEMM_BF16, 0.0, 0.0);
       return DASH_ERR_CUDA;
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    const WInst k = inst_of(a.fmt, plan.bn, plan.parts);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (plan.units < pairs ? plan.units : pairs)), 1, 1);
     cfg.blockDim = dim3(W_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem_of(plan.parts);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kernel_of(a.fmt, plan.parts), tA, tQ, p);
+    cfg.dynamicSmemBytes = k.smem;
+    cfg.numAttrs = attrs(at, true);
+    err = cudaLaunchKernelEx(&cfg, k.k, tA, tQ, p);
   }
   const int tiles = plan.tiles_m * plan.tiles_n;
   if (a.rows == 0) {
@@ -872,20 +1124,13 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
   }
   if (err == cudaSuccess && p.full < tiles) {
     const int n = tiles - p.full;
-    const long long need = static_cast<long long>(n) * (WT * WT / 4 / 256);
+    const long long need = static_cast<long long>(n) * (WM * plan.bn / 4 / 256);
     const long long cap = static_cast<long long>(device_sm_count()) * 8;
-    weight_grad_join_kernel<<<static_cast<unsigned>(need < cap ? need : cap), 256, 0, st>>>(
-        p, p.full, n);
-    err = cudaGetLastError();
-  }
-  const long long r0 = static_cast<long long>(plan.tiles_m) * WT;
-  const long long c0 = static_cast<long long>(plan.tiles_n) * WT;
-  const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
-  if (err == cudaSuccess && (r0 < pr || c0 < pc)) {
-    const dim3 grid(static_cast<unsigned>((pc + 1023) / 1024),
-                    static_cast<unsigned>(pr < 8192 ? pr : 8192));
-    weight_grad_pad_kernel<<<grid, 256, 0, st>>>(a, r0, c0);
-    err = cudaGetLastError();
+    cfg.gridDim = dim3(static_cast<unsigned>(need < cap ? need : cap));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = attrs(at, false);
+    err = cudaLaunchKernelEx(&cfg, weight_grad_join_kernel, p, p.full, n);
   }
   const double t = static_cast<double>(a.rows), o = static_cast<double>(a.outs),
                i = static_cast<double>(a.cols);

@@ -495,6 +495,50 @@ def test_weight_grad_matches_oracle(shape, dtype):
     assert dr.device_status() == 0
 
 
+# Tiles for more than one round of the CTA pairs and a token-split tail, one and several
+# parts, both accumulations.
+WG_LARGE = [(2048, 2304, 2304, torch.bfloat16, torch.bfloat16, "int8"),
+            (2048, 2304, 2304, torch.bfloat16, torch.bfloat16, "e4m3"),
+            (4100, 2200, 1090, torch.bfloat16, torch.float32, "int8"),
+            (2048, 2304, 2304, torch.float16, torch.float16, "int8"),
+            (2048, 2304, 1152, torch.float32, torch.float32, "e4m3"),
+            (8192, 5632, 2048, torch.bfloat16, torch.bfloat16, "int8")]
+
+
+@pytest.mark.parametrize("rows,outs,cols,dtype,odt,fmt", WG_LARGE)
+def test_weight_grad_over_many_tiles_every_run(rows, outs, cols, dtype, odt, fmt):
+    """Many tiles per CTA pair, run again and again: every run gives the same bits, within
+    a bound that one wrong token in one tile would break.
+
+    The bound.  An instruction adds 16 tokens of one part to the running sum S and loses at
+    most two units in the last place of the larger of |S| and the slice's sum of
+    magnitudes; |S| is followed in float64, slot by slot.  One token's product is near 1,
+    the bound below 0.25 before the rounding to dW's type."""
+    require_gpu()
+    dr = library()
+    q, s = dr.act_compress(randn((rows, cols), 60), fmt)
+    dz = randn((rows, outs), 61, dtype)
+    n64, dz64 = dr.act_restore(q, s, cols, fmt, torch.float32).double(), dz.double()
+    want = torch.zeros((outs, cols), dtype=torch.float64, device="cuda")
+    top = torch.zeros_like(want)
+    for t in range(0, rows, 64):
+        a, b = dz64[t:t + 64].t(), n64[t:t + 64]
+        want += a @ b
+        top = torch.maximum(top, want.abs() + a.abs() @ b.abs())
+    steps = PARTS[dtype] * (-(-rows // 16)) + 16
+    bound = 4 * U * steps * top
+    assert float(bound.max()) < 0.25
+    bound = bound + HALF_ULP[odt] * (want.abs() + bound) + TINY[odt]
+    first, _ = dr.weight_grad(dz, q, s, cols, fmt, dtype=odt)
+    assert ((first.double() - want).abs() <= bound).all()
+    ws = torch.empty(dr.weight_grad_workspace_size(rows, outs, cols, dtype, out_dtype=odt),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(24):
+        again, _ = dr.weight_grad(dz, q, s, cols, fmt, dtype=odt, ws=ws)
+        assert (again == first).all()
+    assert dr.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_weight_grad_of_strided_views(dtype):
     require_gpu()

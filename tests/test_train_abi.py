@@ -94,10 +94,11 @@ def test_weight_grad_refusals():
     assert wgrad(lib, outs=1 << 23, lddz=1 << 23, cols=1 << 23, ldw=1 << 23) == INVALID
     n = ctypes.c_size_t(0)
     size = lib.dash_weight_grad_workspace_size
-    assert size(4, 4, -1, 1, 0, 0, ctypes.byref(n)) == INVALID
-    assert size(4, 4, 4, 7, 0, 0, ctypes.byref(n)) == INVALID
-    assert size(4, 4, 4, 1, 0, 100, ctypes.byref(n)) == INVALID
-    assert size(4, 4, 4, 1, 0, 0, None) == INVALID
+    assert size(4, 4, -1, 1, 1, 0, 0, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 7, 1, 0, 0, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 1, 9, 0, 0, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 1, 1, 0, 100, ctypes.byref(n)) == INVALID
+    assert size(4, 4, 4, 1, 1, 0, 0, None) == INVALID
 
 
 def test_format_names():
