@@ -1,9 +1,9 @@
 // 8-bit activation checkpoints: a matrix to codes and scales, and back.
 //
-// Both are one pass over the data, bound by HBM.  A thread holds Q8_U vectors of eight
-// columns (four neighbouring lanes share a group, so its largest magnitude takes two
-// shuffles) and issues all their loads before the first use.  Q8_U is 4, about 16 to 32
-// KB of reads in flight per 256 threads.
+// Both are one pass over the data, bound by HBM.  A thread holds vectors of eight columns
+// (four neighbouring lanes share a group, so its largest magnitude takes two shuffles) and
+// issues all their loads before the first use: Q8_U of them, 16 to 32 KB of reads in
+// flight per 256 threads.
 #include "act_q8.cuh"
 #include "dash_internal.h"
 #include "train_internal.h"
@@ -13,29 +13,88 @@ namespace dash {
 constexpr int Q8_THREADS = 256;
 constexpr int Q8_U = 4;
 
-// Vector i of a (rows, nv) grid of vectors: FLAT when rows lie without gaps, so that i
-// alone addresses it; else row and column come from a division, 32-bit within a CTA's
-// tile, whose first vector's row and column are (row0, v0).
-struct VecAt {
-  long long row;
-  int v;
-};
-template <bool FLAT>
-__device__ __forceinline__ VecAt vec_at(long long i, long long row0, unsigned v0, unsigned off,
-                                        unsigned nv) {
-  VecAt a;
-  if (FLAT) {
-    a.row = 0;
-    a.v = 0;
-  } else {
-    const unsigned k = (v0 + off) / nv;
-    a.row = row0 + k;
-    a.v = static_cast<int>(v0 + off - k * nv);
+// out = the N words that start `bytes` (0 .. 15) into the words w (N + 4 of them).
+template <int N>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], uint32_t bytes,
+                                            uint32_t (&out)[N]) {
+  if (bytes & 8u) {
+#pragma unroll
+    for (int k = 0; k < N + 2; ++k) w[k] = w[k + 2];
   }
-  return a;
+  if (bytes & 4u) {
+#pragma unroll
+    for (int k = 0; k < N + 1; ++k) w[k] = w[k + 1];
+  }
+  const uint32_t r = (bytes & 3u) * 8u;
+#pragma unroll
+  for (int k = 0; k < N; ++k) out[k] = __funnelshift_r(w[k], w[k + 1], r);
 }
 
-template <typename T, bool VEC, bool FLAT>
+// Eight elements to columns c .. c + 7 of a row at any address; lane l of the warp has
+// columns c0 + 8 l, and the whole warp calls.  A lane stores the aligned 16-byte words that
+// begin in its elements, with the next lane's first bytes; what a warp or a row begins or
+// ends with goes singly.  (All of it singly: 63 against 31 us for act_restore of
+// 13696 x 1603 bf16.)
+template <typename T>
+__device__ __forceinline__ void store8_joined(T* row, int c, int cols, const F2 (&v)[4]) {
+  constexpr int N = static_cast<int>(sizeof(T)) * 2;
+  constexpr int B = 8 * static_cast<int>(sizeof(T));
+  const uintptr_t r1 = reinterpret_cast<uintptr_t>(row) + cols * sizeof(T);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + static_cast<uintptr_t>(c) * sizeof(T);
+  const uint32_t off = static_cast<uint32_t>(at & 15u);
+  uint32_t w[N + 4], out[N];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      float lo, hi;
+      f2_get(v[k], lo, hi);
+      w[2 * k] = __float_as_uint(lo);
+      w[2 * k + 1] = __float_as_uint(hi);
+    } else {
+      w[k] = pack2<T>(v[k]);
+    }
+  }
+  const int lane = threadIdx.x & 31;
+  const uint32_t head = off ? 16u - off : 0u;  // own bytes before the first boundary
+  const uintptr_t f = at + head;
+  // Whether this lane stores whole words [f, f + B), and whether the lane before does (its
+  // words end at f and hold this lane's head).
+  const bool whole = f + B <= r1 && (off == 0 || lane < 31);
+  const bool covered = off == 0 || (lane > 0 && f <= r1);
+  uint32_t own[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) own[k] = w[k];
+  if (off != 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[N + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
+    shift_words<N>(w, head, out);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) out[k] = w[k];
+  }
+  if (whole)
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+      *reinterpret_cast<uint4*>(f + 4 * k) = make_uint4(out[k], out[k + 1], out[k + 2], out[k + 3]);
+  if (!whole || !covered) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uintptr_t e = at + k * sizeof(T);
+      if (e < r1 && (e < f ? !covered : !whole)) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<uint32_t*>(e) = own[k];
+        else
+          *reinterpret_cast<uint16_t*>(e) =
+              static_cast<uint16_t>(own[k / 2] >> (16 * (k & 1)));
+      }
+    }
+  }
+}
+
+// Vector i of the padded matrix, nv vectors a row.  FLAT (rows of whole groups, without
+// gaps): i alone addresses it.  Else its row and column come from a 32-bit division within
+// the CTA's tile, whose first vector has row row0 and place v0 in it.
+template <typename T, int MODE, bool FLAT>
 __global__ void __launch_bounds__(Q8_THREADS)
     act_compress_kernel(const CompressArgs a, unsigned nv, long long total) {
   const long long base = static_cast<long long>(blockIdx.x) * (Q8_THREADS * Q8_U);
@@ -47,9 +106,13 @@ __global__ void __launch_bounds__(Q8_THREADS)
   for (int u = 0; u < Q8_U; ++u) {
     const unsigned off = u * Q8_THREADS + threadIdx.x;
     const long long i = base + off;
-    const VecAt at = vec_at<FLAT>(i, row0, v0, off, nv);
-    const int left = i >= total ? 0 : (FLAT ? 8 : static_cast<int>(min(a.cols - at.v * 8LL, 8LL)));
-    load8<T, VEC>(x + (FLAT ? i * 8 : at.row * a.ld + at.v * 8LL), left, v[u]);
+    if (FLAT) {
+      load8_vec<T>(x + i * 8, i < total ? 8 : 0, v[u]);
+    } else {
+      const unsigned k = (v0 + off) / nv;
+      const int c = static_cast<int>(v0 + off - k * nv) * 8;
+      load8<T, MODE>(x + (row0 + k) * a.ld, c, i < total ? static_cast<int>(a.cols) : c, v[u]);
+    }
   }
 #pragma unroll
   for (int u = 0; u < Q8_U; ++u) {
@@ -64,115 +127,132 @@ __global__ void __launch_bounds__(Q8_THREADS)
   }
 }
 
-template <typename T, bool VEC, bool FLAT>
+// FLAT as above.  Else a warp holds 32 neighbouring vectors of one row: unit i is row
+// i / units and the columns from 256 (i % units) on.
+template <typename T, int MODE, bool FLAT>
 __global__ void __launch_bounds__(Q8_THREADS)
-    act_restore_kernel(const RestoreArgs a, unsigned nv, long long total) {
-  const long long base = static_cast<long long>(blockIdx.x) * (Q8_THREADS * Q8_U);
-  const long long row0 = FLAT ? 0 : base / nv;
-  const unsigned v0 = FLAT ? 0 : static_cast<unsigned>(base - row0 * nv);
+    act_restore_kernel(const RestoreArgs a, unsigned units, long long total) {
   T* x = static_cast<T*>(a.x);
+  const long long pitch = (a.cols + Q8_GROUP - 1) / Q8_GROUP * Q8_GROUP;
+  const int lane = threadIdx.x & 31;
+  long long row[Q8_U], col[Q8_U];
+  bool in[Q8_U];
   uint2 codes[Q8_U];
   uint32_t b[Q8_U];
 #pragma unroll
   for (int u = 0; u < Q8_U; ++u) {
-    const long long i = base + u * Q8_THREADS + threadIdx.x;
+    if (FLAT) {
+      const long long i =
+          (static_cast<long long>(blockIdx.x) * Q8_U + u) * Q8_THREADS + threadIdx.x;
+      row[u] = 0;
+      col[u] = i * 8;
+      in[u] = i < total;
+    } else {
+      const long long i = (static_cast<long long>(blockIdx.x) * Q8_U + u) * (Q8_THREADS / 32) +
+                          (threadIdx.x >> 5);
+      row[u] = total < (1LL << 32) ? static_cast<unsigned>(i) / units : i / units;
+      col[u] = (i - row[u] * units) * 256 + lane * 8;
+      in[u] = i < total;
+    }
     codes[u] = make_uint2(0u, 0u);
     b[u] = 127u;
-    if (i < total) {
-      codes[u] = reinterpret_cast<const uint2*>(a.q)[i];
-      b[u] = a.scale[i >> 2];
+    if (in[u] && (FLAT || col[u] < pitch)) {
+      const long long at = row[u] * pitch + col[u];
+      codes[u] = *reinterpret_cast<const uint2*>(a.q + at);
+      b[u] = a.scale[at / Q8_GROUP];
     }
   }
 #pragma unroll
   for (int u = 0; u < Q8_U; ++u) {
-    const unsigned off = u * Q8_THREADS + threadIdx.x;
-    const long long i = base + off;
-    const VecAt at = vec_at<FLAT>(i, row0, v0, off, nv);
-    const int left = i >= total ? 0 : (FLAT ? 8 : static_cast<int>(min(a.cols - at.v * 8LL, 8LL)));
     F2 v[4];
     if (a.fmt == DASH_Q8_INT8)
       q8_decode8<DASH_Q8_INT8>(codes[u], b[u], v);
     else
       q8_decode8<DASH_Q8_E4M3>(codes[u], b[u], v);
-    store8<T, VEC>(x + (FLAT ? i * 8 : at.row * a.ld + at.v * 8LL), left, v);
+    if (FLAT) {
+      store8_vec<T>(x + col[u], in[u] ? 8 : 0, v);
+    } else if (in[u]) {  // the same for the whole warp
+      T* to = x + row[u] * a.ld;
+      const int c = static_cast<int>(col[u]), cols = static_cast<int>(a.cols);
+      if constexpr (MODE == ACC_ANY)
+        store8_joined<T>(to, c, cols, v);
+      else
+        store8_vec<T>(to + c, cols - c, v);
+    }
   }
 }
 
-// Access of a (rows, cols) matrix: eight-column vectors where address, leading dimension
-// and width allow them (2); without gaps between rows of whole groups besides (3); else
-// single elements (0).
-static int access_mode(const void* x, int dt, long long cols, long long ld) {
-  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && cols % 8 == 0 &&
-                   (ld * dt_bytes(dt)) % 16 == 0;
-  return vec ? (ld == cols && cols % Q8_GROUP == 0 ? 3 : 2) : 0;
+// How a matrix is reached: rows of whole groups without gaps as one long row (flat), by
+// vectors of eight where address, leading dimension and width allow them, or anyhow.
+struct Reach {
+  bool flat, vec;
+};
+static Reach reach(const void* x, int dt, long long cols, long long ld) {
+  const bool vec = cols % 8 == 0 && vec_ok(x, ld, dt);
+  return {vec && ld == cols && cols % Q8_GROUP == 0, vec};
+}
+// CTAs for n units, `per` of them each; 0 where a grid cannot hold them.
+static unsigned ctas(long long n, int per) {
+  const long long g = (n + per - 1) / per;
+  return g <= 0x7fffffff ? static_cast<unsigned>(g) : 0;
 }
 
 template <typename T>
-static void compress_t(const CompressArgs& a, int mode, unsigned grid, unsigned nv,
-                       long long total, cudaStream_t st) {
-  if (mode == 3)
-    act_compress_kernel<T, true, true><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
-  else if (mode == 2)
-    act_compress_kernel<T, true, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+static bool compress_t(const CompressArgs& a, cudaStream_t st) {
+  const Reach r = reach(a.x, a.dt, a.cols, a.ld);
+  const unsigned nv = static_cast<unsigned>((a.cols + Q8_GROUP - 1) / Q8_GROUP * 4);
+  const long long total = a.rows * nv;
+  const unsigned g = ctas(total, Q8_THREADS * Q8_U);
+  if (g == 0) return false;
+  if (r.flat)
+    act_compress_kernel<T, ACC_VEC, true><<<g, Q8_THREADS, 0, st>>>(a, nv, total);
+  else if (r.vec)
+    act_compress_kernel<T, ACC_VEC, false><<<g, Q8_THREADS, 0, st>>>(a, nv, total);
   else
-    act_compress_kernel<T, false, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+    act_compress_kernel<T, ACC_ANY, false><<<g, Q8_THREADS, 0, st>>>(a, nv, total);
+  return true;
 }
 
 template <typename T>
-static void restore_t(const RestoreArgs& a, int mode, unsigned grid, unsigned nv,
-                      long long total, cudaStream_t st) {
-  if (mode == 3)
-    act_restore_kernel<T, true, true><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
-  else if (mode == 2)
-    act_restore_kernel<T, true, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+static bool restore_t(const RestoreArgs& a, cudaStream_t st) {
+  const Reach r = reach(a.x, a.dt, a.cols, a.ld);
+  const unsigned units = static_cast<unsigned>((a.cols + 255) / 256);
+  const long long total = r.flat ? a.rows * (a.cols / 8) : a.rows * units;
+  const unsigned g = ctas(total, r.flat ? Q8_THREADS * Q8_U : Q8_THREADS / 32 * Q8_U);
+  if (g == 0) return false;
+  if (r.flat)
+    act_restore_kernel<T, ACC_VEC, true><<<g, Q8_THREADS, 0, st>>>(a, units, total);
+  else if (r.vec)
+    act_restore_kernel<T, ACC_VEC, false><<<g, Q8_THREADS, 0, st>>>(a, units, total);
   else
-    act_restore_kernel<T, false, false><<<grid, Q8_THREADS, 0, st>>>(a, nv, total);
+    act_restore_kernel<T, ACC_ANY, false><<<g, Q8_THREADS, 0, st>>>(a, units, total);
+  return true;
 }
 
-// Vectors of the padded matrix, and the CTAs that hold them; false where the grid cannot.
-static bool vec_grid(long long rows, long long cols, unsigned& nv, long long& total,
-                     unsigned& grid) {
-  nv = static_cast<unsigned>((cols + Q8_GROUP - 1) / Q8_GROUP * 4);
-  total = rows * nv;
-  const long long g = (total + Q8_THREADS * Q8_U - 1) / (Q8_THREADS * Q8_U);
-  grid = static_cast<unsigned>(g);
-  return g <= 0x7fffffff;
+static double code_bytes(long long rows, long long cols) {
+  return static_cast<double>(rows) * ((cols + Q8_GROUP - 1) / Q8_GROUP) * (Q8_GROUP + 1);
 }
 
 dash_status launch_act_compress(const CompressArgs& a, cudaStream_t st) {
-  unsigned nv, grid;
-  long long total;
-  if (!vec_grid(a.rows, a.cols, nv, total, grid)) return DASH_ERR_UNSUPPORTED;
-  const int mode = access_mode(a.x, a.dt, a.cols, a.ld);
   const int rec = trace_begin(st);
-  if (a.dt == DASH_DT_F32)
-    compress_t<float>(a, mode, grid, nv, total, st);
-  else if (a.dt == DASH_DT_BF16)
-    compress_t<__nv_bfloat16>(a, mode, grid, nv, total, st);
-  else
-    compress_t<__half>(a, mode, grid, nv, total, st);
+  const bool ok = a.dt == DASH_DT_F32    ? compress_t<float>(a, st)
+                  : a.dt == DASH_DT_BF16 ? compress_t<__nv_bfloat16>(a, st)
+                                         : compress_t<__half>(a, st);
   const cudaError_t err = cudaGetLastError();
   trace_end(rec, st, DASH_TRACE_CHECKPOINT, 0.0,
-            static_cast<double>(a.rows) * (a.cols * dt_bytes(a.dt) + nv * 8.25));
-  return err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+            static_cast<double>(a.rows) * a.cols * dt_bytes(a.dt) + code_bytes(a.rows, a.cols));
+  return !ok ? DASH_ERR_UNSUPPORTED : (err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA);
 }
 
 dash_status launch_act_restore(const RestoreArgs& a, cudaStream_t st) {
-  unsigned nv, grid;
-  long long total;
-  if (!vec_grid(a.rows, a.cols, nv, total, grid)) return DASH_ERR_UNSUPPORTED;
-  const int mode = access_mode(a.x, a.dt, a.cols, a.ld);
   const int rec = trace_begin(st);
-  if (a.dt == DASH_DT_F32)
-    restore_t<float>(a, mode, grid, nv, total, st);
-  else if (a.dt == DASH_DT_BF16)
-    restore_t<__nv_bfloat16>(a, mode, grid, nv, total, st);
-  else
-    restore_t<__half>(a, mode, grid, nv, total, st);
+  const bool ok = a.dt == DASH_DT_F32    ? restore_t<float>(a, st)
+                  : a.dt == DASH_DT_BF16 ? restore_t<__nv_bfloat16>(a, st)
+                                         : restore_t<__half>(a, st);
   const cudaError_t err = cudaGetLastError();
   trace_end(rec, st, DASH_TRACE_CHECKPOINT, 0.0,
-            static_cast<double>(a.rows) * (a.cols * dt_bytes(a.dt) + nv * 8.25));
-  return err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+            static_cast<double>(a.rows) * a.cols * dt_bytes(a.dt) + code_bytes(a.rows, a.cols));
+  return !ok ? DASH_ERR_UNSUPPORTED : (err == cudaSuccess ? DASH_OK : DASH_ERR_CUDA);
 }
 
 }  // namespace dash

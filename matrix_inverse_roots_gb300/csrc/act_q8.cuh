@@ -172,58 +172,82 @@ __device__ __forceinline__ uint32_t pack2(F2 a) {
     return pack_half2(lo, hi);
 }
 
-// Eight elements from p, of which `n` exist (any n; <= 0: none); the others are zero.
-// VEC: p is 16-byte aligned and none or all of the eight exist.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, F2 (&v)[4]) {
-  if constexpr (!VEC) {
+// How a thread's eight columns are reached: by one access (two for fp32) of which none or
+// all exist, at a 16-byte boundary; or in a row of any width at any address.
+enum Access : int { ACC_ANY = 0, ACC_VEC = 1, ACC_FULL = 2 };  // FULL: all exist
+
+// Eight elements from p at any address, of which n exist; the others are zero.  (Read
+// singly: L1 serves a warp's 512 bytes to its eight loads.  Aligned 16-byte loads whose
+// words are shifted and joined across lanes took longer: 33 against 20 us for act_compress
+// of 13696 x 1603 bf16, 116 against 87 us for the norm's backward pass.)
+template <typename T>
+__device__ __forceinline__ void load8_any(const T* p, int n, F2 (&v)[4]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = f2(2 * k < n ? Elem<T>::to(p[2 * k]) : 0.0f,
-                2 * k + 1 < n ? Elem<T>::to(p[2 * k + 1]) : 0.0f);
-  } else {
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    if (n > 0) {
-      a = reinterpret_cast<const uint4*>(p)[0];
-      if constexpr (sizeof(T) == 4) b = reinterpret_cast<const uint4*>(p)[1];
-    }
-    if constexpr (sizeof(T) == 4) {
-      v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
-      v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
-      v[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y));
-      v[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
-    } else {
-      v[0] = unpack2<T>(a.x);
-      v[1] = unpack2<T>(a.y);
-      v[2] = unpack2<T>(a.z);
-      v[3] = unpack2<T>(a.w);
-    }
+  for (int k = 0; k < 4; ++k)
+    v[k] = f2(2 * k < n ? Elem<T>::to(p[2 * k]) : 0.0f,
+              2 * k + 1 < n ? Elem<T>::to(p[2 * k + 1]) : 0.0f);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8_any(T* p, int n, const F2 (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    f2_get(v[k], lo, hi);
+    if (2 * k < n) p[2 * k] = Elem<T>::from(lo);
+    if (2 * k + 1 < n) p[2 * k + 1] = Elem<T>::from(hi);
   }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const F2 (&v)[4]) {
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float lo, hi;
-      f2_get(v[k], lo, hi);
-      if (2 * k < n) p[2 * k] = Elem<T>::from(lo);
-      if (2 * k + 1 < n) p[2 * k + 1] = Elem<T>::from(hi);
-    }
-  } else {
-    if (n <= 0) return;
-    if constexpr (sizeof(T) == 4) {
-      float f[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) f2_get(v[k], f[2 * k], f[2 * k + 1]);
-      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-      *reinterpret_cast<uint4*>(p) =
-          make_uint4(pack2<T>(v[0]), pack2<T>(v[1]), pack2<T>(v[2]), pack2<T>(v[3]));
-    }
+// Eight elements from p, at a 16-byte boundary; zeros unless n > 0.
+template <typename T>
+__device__ __forceinline__ void load8_vec(const T* p, int n, F2 (&v)[4]) {
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+  if (n > 0) {
+    a = reinterpret_cast<const uint4*>(p)[0];
+    if constexpr (sizeof(T) == 4) b = reinterpret_cast<const uint4*>(p)[1];
   }
+  if constexpr (sizeof(T) == 4) {
+    v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
+    v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
+    v[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y));
+    v[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
+  } else {
+    v[0] = unpack2<T>(a.x);
+    v[1] = unpack2<T>(a.y);
+    v[2] = unpack2<T>(a.z);
+    v[3] = unpack2<T>(a.w);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8_vec(T* p, int n, const F2 (&v)[4]) {
+  if (n <= 0) return;
+  if constexpr (sizeof(T) == 4) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f2_get(v[k], f[2 * k], f[2 * k + 1]);
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2<T>(v[0]), pack2<T>(v[1]), pack2<T>(v[2]), pack2<T>(v[3]));
+  }
+}
+
+// Columns c .. c + 7 of a row, either way.
+template <typename T, int MODE>
+__device__ __forceinline__ void load8(const T* row, int c, int cols, F2 (&v)[4]) {
+  if constexpr (MODE == ACC_ANY)
+    load8_any<T>(row + c, cols - c, v);
+  else
+    load8_vec<T>(row + c, MODE == ACC_FULL ? 8 : cols - c, v);
+}
+template <typename T, int MODE>
+__device__ __forceinline__ void store8(T* row, int c, int cols, const F2 (&v)[4]) {
+  if constexpr (MODE == ACC_ANY)
+    store8_any<T>(row + c, cols - c, v);
+  else
+    store8_vec<T>(row + c, MODE == ACC_FULL ? 8 : cols - c, v);
 }
 
 // The value after a round trip through T.
@@ -235,17 +259,18 @@ __device__ __forceinline__ F2 round2(F2 a) {
     return unpack2<T>(pack2<T>(a));
 }
 
-// Eight elements of a per-column vector whose type is a run-time argument.  vec: the
-// vector is 16-byte aligned and none or all of the eight exist.
+// Eight elements, from i on, of a per-column vector whose type is a run-time argument, of
+// which n exist; the others are zero.  vec: the vector lies at a 16-byte boundary (and i is
+// a multiple of eight).
 __device__ __forceinline__ void load8_dt(const void* p, int dt, bool vec, int64_t i, int n,
                                          F2 (&v)[4]) {
-  if (vec) {
+  if (vec && n >= 8) {
     if (dt == DASH_DT_F32)
-      load8<float, true>(static_cast<const float*>(p) + i, n, v);
+      load8_vec<float>(static_cast<const float*>(p) + i, 8, v);
     else if (dt == DASH_DT_BF16)
-      load8<__nv_bfloat16, true>(static_cast<const __nv_bfloat16*>(p) + i, n, v);
+      load8_vec<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(p) + i, 8, v);
     else
-      load8<__half, true>(static_cast<const __half*>(p) + i, n, v);
+      load8_vec<__half>(static_cast<const __half*>(p) + i, 8, v);
     return;
   }
 #pragma unroll

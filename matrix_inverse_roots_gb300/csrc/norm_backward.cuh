@@ -1,0 +1,309 @@
+// The norm's backward pass: the kernel and its launch, instantiated per element type in
+// norm_backward_{f32,bf16,f16}.cu (one translation unit each, so that they compile side by
+// side).
+#pragma once
+
+#include "dash_internal.h"
+#include "norm_common.cuh"
+#include "train_internal.h"
+
+namespace dash {
+
+// Joins the groups' column sums, in order, into row blockIdx.x of `part` (dgamma's sums,
+// then dbeta's).  sums: 2 cols floats of shared memory.
+template <int J>
+__device__ __forceinline__ void join_groups(float* sums, float* part, int cols, int W, int G,
+                                            int grp, int t, const F2 (&dg)[J][4],
+                                            const F2 (&db)[J][4]) {
+  float* out = part + static_cast<long long>(blockIdx.x) * 2 * cols;
+  for (int i = 0; i < G; ++i) {
+    if (grp == i) {
+      float* to = i + 1 < G ? sums : out;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int c = (j * 32 * W + t) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float g[2], b[2];
+          f2_get(dg[j][k], g[0], g[1]);
+          f2_get(db[j][k], b[0], b[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = c + 2 * k + h;
+            if (col >= cols) continue;
+            if (i > 0) {
+              g[h] += sums[col];
+              b[h] += sums[cols + col];
+            }
+            to[col] = g[h];
+            to[cols + col] = b[h];
+          }
+        }
+      }
+    }
+    if (i + 1 < G) __syncthreads();
+  }
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// W warps per row, G groups of them per CTA; with the ring, S stages of `stage` bytes for
+// each group.  goff: the offset of gamma's copy in dynamic shared memory; gvec: gamma
+// itself lies at a 16-byte boundary.
+struct RowPlan {
+  int W, G, S;
+  uint32_t stage, goff;
+  bool gvec;
+};
+
+// Where n comes from.
+enum NSource : int { N_FROM_X = 0, N_INT8 = 1, N_E4M3 = 2 };
+// dx = rstd (g - mean(g) - n mean(g n)) + dres, g = dy gamma, and this CTA's share of
+// dgamma = sum dy n and dbeta = sum dy.  Persistent, one CTA per SM: each group takes a row
+// at a time, and a thread keeps its columns from row to row, so that their sums stay in
+// registers and leave once, joined over the groups, as row blockIdx.x of `part`.
+// A row is read twice, before and after its sums.  (Held in registers in between it was
+// slower, 51.6 against 46.8 us at 8192 x 2048: the registers the sums leave are few.)
+// GS: gamma lies in shared memory, in fp32.  Else it is read from where it is: by short or
+// few rows, and by wide ones whose ring needs the room (4096 x 16384 bf16 with dres: 144
+// us; with gamma's copy and no ring 231).
+// RING: a row's inputs come by bulk copies into a ring of shared-memory stages that the
+// group's first thread fills ahead, so that reads are in flight while a row's sums and
+// their barrier are waited for.  A stage is refilled once every thread has read it for the
+// last time, after the next row's barrier.  Without RING (rows of odd sizes or alignment,
+// short or few rows) the threads load for themselves.
+// After a wait that ran out the group carries on (its threads must meet at its barriers)
+// with whatever the stage holds and issues no more copies; the error flag tells.
+// Named barrier 1 + grp is the group's: barrier 0 is the whole CTA's, where groups that
+// have run out of rows wait while others still sum.
+template <typename T, int SRC, int J, int MODE, bool RING, bool GS>
+__global__ void __launch_bounds__(32 * BWD_WARPS, 1)
+    norm_backward_kernel(const NormBwdArgs a, const RowPlan p, float* part) {
+  constexpr bool CK = SRC != N_FROM_X;
+  __shared__ float red[BWD_WARPS][2][2 * 32];
+  __shared__ int abort_s;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = p.W, grp = warp / W, wr = warp - grp * W, t = wr * 32 + lane;
+  const bool first = t == 0;
+  const uint32_t bars = smem_u32(dyn) + 8u * (grp * p.S), data = smem_u32(dyn) + RING_BARS;
+  volatile int* abort_flag = &abort_s;
+  float* gs = reinterpret_cast<float*>(dyn + p.goff);
+  if (RING && threadIdx.x == 0) {
+    abort_s = 0;
+    for (int i = 0; i < p.G * p.S; ++i) mbar_init(smem_u32(dyn) + 8u * i, 1);
+    fence_barrier_init();
+  }
+  if (GS)
+    for (int c = threadIdx.x; c < (a.cols + 7) / 8 * 8; c += blockDim.x)
+      gs[c] = a.gamma && c < a.cols ? load_dt(a.gamma, a.wdt, c) : 1.0f;
+  __syncthreads();
+  const int rows = static_cast<int>(a.rows);
+  const uint32_t step = gridDim.x * p.G, row0 = blockIdx.x * p.G + grp;
+  const int ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP, pitch = ng * Q8_GROUP;
+  const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  const uint32_t nbytes = CK ? static_cast<uint32_t>(pitch) : bytes;
+  // A stage: dy, x or the codes, dres.
+  auto fill = [&](uint32_t row, int s) {
+    if (row >= static_cast<uint32_t>(rows) || *abort_flag) return;
+    const long long r = row;
+    const uint32_t bar = bars + 8u * s;
+    const uint32_t dst = data + (grp * p.S + s) * p.stage;
+    mbar_arrive_expect_tx(bar, bytes + nbytes + (a.dres ? bytes : 0u));
+    bulk_load(dst, static_cast<const T*>(a.dy) + r * a.lddy, bytes, bar);
+    if (CK)
+      bulk_load(dst + bytes, a.q + r * pitch, nbytes, bar);
+    else
+      bulk_load(dst + bytes, static_cast<const T*>(a.x) + r * a.ldx, nbytes, bar);
+    if (a.dres)
+      bulk_load(dst + bytes + nbytes, static_cast<const T*>(a.dres) + r * a.lddres, bytes, bar);
+  };
+  if (RING && first)
+    for (int s = 0; s < p.S; ++s) fill(row0 + s * step, s);
+  const int c0 = t * 8, cstep = 256 * W;  // columns c0 + j cstep
+  // Columns of vector j that exist.
+  auto left = [&](int j) { return MODE == ACC_FULL ? 8 : a.cols - (c0 + j * cstep); };
+  F2 dg[J][4], db[J][4];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dg[j][k] = db[j][k] = f2(0.0f);
+  // Scales and statistics come straight from global memory, one row ahead.
+  constexpr int NSC = CK ? J : 1;
+  uint32_t sc[NSC] = {};
+  float rstd = 0.0f, mean = 0.0f;
+  auto small = [&](uint32_t row, uint32_t (&b)[NSC], float& rs, float& mu) {
+    if constexpr (CK) {
+      const uint8_t* sp = a.scale + static_cast<long long>(row) * ng + t / 4;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        b[j] = MODE == ACC_FULL || c0 + j * cstep < pitch ? sp[j * (cstep / 32)] : 127u;
+    } else if (a.center) {
+      mu = a.mean[row];
+    }
+    rs = a.rstd[row];
+  };
+  if (row0 < static_cast<uint32_t>(rows)) small(row0, sc, rstd, mean);
+  const float inv = 1.0f / a.cols;
+  const bool has_db = a.dbeta != nullptr;
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  for (uint32_t row = row0; row < static_cast<uint32_t>(rows); row += step) {
+    uint32_t nsc[NSC] = {};
+    float nrstd = 0.0f, nmean = 0.0f;
+    if (row + step < static_cast<uint32_t>(rows)) small(row + step, nsc, nrstd, nmean);
+    const long long r = row;
+    const uint8_t* st = dyn + RING_BARS + (grp * p.S + s) * p.stage;
+    if (RING) mbar_wait(bars + 8u * s, ph, abort_flag);
+    const T* dyp = RING ? reinterpret_cast<const T*>(st)
+                        : static_cast<const T*>(a.dy) + r * a.lddy;
+    const T* xp = RING ? reinterpret_cast<const T*>(st + bytes)
+                       : static_cast<const T*>(a.x) + (CK ? 0 : r * a.ldx);
+    const uint8_t* qp = RING ? st + bytes : a.q + (CK ? r * pitch : 0);
+    const F2 rs = f2(rstd), less = f2(-mean);
+    // Vector j: dy and n.
+    auto vector8 = [&](int j, F2 (&d)[4], F2 (&m)[4]) {
+      const int c = c0 + j * cstep;
+      load8<T, MODE>(dyp, c, a.cols, d);
+      if constexpr (CK) {
+        uint2 q = make_uint2(0u, 0u);
+        if (MODE != ACC_ANY || c < pitch) q = *reinterpret_cast<const uint2*>(qp + c);
+        q8_decode8<SRC == N_INT8 ? DASH_Q8_INT8 : DASH_Q8_E4M3>(q, sc[j], m);
+      } else {
+        load8<T, MODE>(xp, c, a.cols, m);
+        // The difference first: x may lie far from zero.
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = (m[k] + less) * rs;
+      }
+    };
+    auto scale8 = [&](int j, F2 (&d)[4]) {
+      F2 w[4];
+      const int c = c0 + j * cstep;
+      if constexpr (GS) {
+        load8_vec<float>(gs + c, left(j), w);
+      } else if (a.gamma) {
+        load8_dt(a.gamma, a.wdt, p.gvec, c, left(j), w);
+      } else {
+        return;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = d[k] * w[k];
+    };
+    F2 s1 = f2(0.0f), s2 = f2(0.0f);
+    // Columns outside the row have dy = g = 0 and add nothing to any sum: n is finite
+    // there (it is -mean rstd, or a padding code), unless the row is not finite anyway.
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (MODE == ACC_VEC && left(j) <= 0) continue;
+      F2 gj[4], nj[4];
+      vector8(j, gj, nj);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        dg[j][k] = f2_fma(gj[k], nj[k], dg[j][k]);
+        if (has_db) db[j][k] = db[j][k] + gj[k];
+      }
+      scale8(j, gj);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s1 = s1 + gj[k];
+        s2 = f2_fma(gj[k], nj[k], s2);
+      }
+    }
+    // The sums' buffers alternate: a slow warp may still read one row's when another
+    // writes the next row's.
+    float sum[2] = {f2_sum(s1), f2_sum(s2)};
+    row_sum<2>(sum, W, wr, red[grp][flip], 1 + grp);
+    flip ^= 1;
+    if (RING) {
+      if (W == 1) __syncwarp();
+      if (first && row != row0) fill(row + (p.S - 1) * step, s == 0 ? p.S - 1 : s - 1);
+    }
+    const F2 m1 = f2(a.center ? -sum[0] * inv : 0.0f), m2 = f2(-sum[1] * inv);
+    T* dxp = static_cast<T*>(a.dx) + r * a.lddx;
+    const T* rp = RING ? reinterpret_cast<const T*>(st + bytes + nbytes)
+                       : static_cast<const T*>(a.dres) + r * a.lddres;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (MODE == ACC_VEC && left(j) <= 0) continue;
+      F2 gj[4], nj[4], rj[4];
+      vector8(j, gj, nj);
+      scale8(j, gj);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gj[k] = f2_fma(nj[k], m2, gj[k] + m1) * rs;
+      if (a.dres) {
+        load8<T, MODE>(rp, c0 + j * cstep, a.cols, rj);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gj[k] = gj[k] + rj[k];
+      }
+      store8<T, MODE>(dxp, c0 + j * cstep, a.cols, gj);
+    }
+    if (RING && ++s == p.S) {
+      s = 0;
+      ph ^= 1u;
+    }
+#pragma unroll
+    for (int j = 0; j < NSC; ++j) sc[j] = nsc[j];
+    rstd = nrstd;
+    mean = nmean;
+  }
+  if (part == nullptr) return;
+  // Every copy has landed and been read, and gamma too: the groups' sums take their place.
+  __syncthreads();
+  join_groups<J>(reinterpret_cast<float*>(dyn), part, a.cols, W, p.G, grp, t, dg, db);
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename T, int SRC, int J, int MODE, bool RING, bool GS>
+dash_status backward_k(const NormBwdArgs& a, const BwdPlan& b, RowPlan p, float* part,
+                       cudaStream_t st) {
+  auto k = norm_backward_kernel<T, SRC, J, MODE, RING, GS>;
+  p.goff = RING ? static_cast<uint32_t>(p.G) * p.S * p.stage + RING_BARS : 0;
+  p.gvec = (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0;
+  size_t smem = p.goff + (GS ? gamma_room(a.cols) : 0);
+  const size_t join = part && p.G > 1 ? static_cast<size_t>(a.cols) * 8 : 0;
+  if (smem < join) smem = join;
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem)) != cudaSuccess)
+    return DASH_ERR_CUDA;
+  k<<<b.grid, 32 * p.W * p.G, smem, st>>>(a, p, part);
+  return cudaGetLastError() == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+template <typename T, int SRC, int J>
+dash_status backward_j(const NormBwdArgs& a, const BwdPlan& b, float* part, cudaStream_t st) {
+  RowPlan p = {b.W, b.G, b.S, b.stage, 0, false};
+  if (!b.vec) return backward_k<T, SRC, J, ACC_ANY, false, true>(a, b, p, part, st);
+  if (b.S == 0) return backward_k<T, SRC, J, ACC_VEC, false, false>(a, b, p, part, st);
+  const bool full = a.cols == 256 * b.W * J;
+  if constexpr (J > 1) {
+    if (!b.gamma_fits)
+      return full ? backward_k<T, SRC, J, ACC_FULL, true, false>(a, b, p, part, st)
+                  : backward_k<T, SRC, J, ACC_VEC, true, false>(a, b, p, part, st);
+  }
+  return full ? backward_k<T, SRC, J, ACC_FULL, true, true>(a, b, p, part, st)
+              : backward_k<T, SRC, J, ACC_VEC, true, true>(a, b, p, part, st);
+}
+
+template <typename T, int SRC>
+dash_status backward_t(const NormBwdArgs& a, const BwdPlan& b, float* part, cudaStream_t st) {
+  return b.J == 4   ? backward_j<T, SRC, 4>(a, b, part, st)
+         : b.J == 2 ? backward_j<T, SRC, 2>(a, b, part, st)
+                    : backward_j<T, SRC, 1>(a, b, part, st);
+}
+
+template <typename T>
+dash_status backward_c(const NormBwdArgs& a, const BwdPlan& b, float* part, cudaStream_t st) {
+  if (a.q == nullptr) return backward_t<T, N_FROM_X>(a, b, part, st);
+  return a.fmt == DASH_Q8_INT8 ? backward_t<T, N_INT8>(a, b, part, st)
+                               : backward_t<T, N_E4M3>(a, b, part, st);
+}
+
+}  // namespace dash

@@ -8,6 +8,12 @@
 
 namespace dash {
 
+inline int dt_bytes(int dt) { return dt == DASH_DT_F32 ? 4 : 2; }
+// Whether 16-byte accesses fit a matrix's rows.
+inline bool vec_ok(const void* p, long long ld, int dt) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * dt_bytes(dt)) % 16 == 0;
+}
+
 struct CompressArgs {
   const void* x;
   int dt;
@@ -77,6 +83,28 @@ struct NormBwdArgs {
   float* dgamma;  // null: not wanted
   float* dbeta;   // null: not wanted
 };
+// How a backward pass is laid out: J vectors per thread, W warps per row, G rows at once
+// per CTA, one persistent CTA per SM; a ring of S stages per row at once (0: none), of
+// `stage` bytes; whether gamma's copy fits beside it, and 16-byte accesses the rows.
+struct BwdPlan {
+  int J, W, G, S, grid;
+  uint32_t stage;
+  bool gamma_fits, vec;
+};
+constexpr int BWD_WARPS = 16;                        // of a backward CTA, at most
+constexpr int RING_MAX = 8;                          // most stages of a group
+constexpr int RING_BARS = 8 * BWD_WARPS * RING_MAX;  // their barriers
+constexpr size_t BWD_SMEM = 208 * 1024;              // dynamic; 16 KB more are static
+inline size_t gamma_room(int cols) { return (static_cast<size_t>(cols) + 7) / 8 * 32; }
+dash_status norm_backward_f32(const NormBwdArgs& a, const BwdPlan& b, float* part,
+                              cudaStream_t st);
+dash_status norm_backward_bf16(const NormBwdArgs& a, const BwdPlan& b, float* part,
+                               cudaStream_t st);
+dash_status norm_backward_f16(const NormBwdArgs& a, const BwdPlan& b, float* part,
+                              cudaStream_t st);
+int norm_f32_read_clear_error();
+int norm_bf16_read_clear_error();
+int norm_f16_read_clear_error();
 size_t norm_backward_ws(long long rows, long long cols);
 dash_status launch_norm_backward(const NormBwdArgs& a, void* ws, cudaStream_t st);
 
@@ -110,6 +138,5 @@ dash_status launch_col_sum(const void* m, int dt, long long rows, long long cols
 dash_status launch_part_sum(const float* part, int parts, long long cols, float* out,
                             cudaStream_t st);
 
-inline int dt_bytes(int dt) { return dt == DASH_DT_F32 ? 4 : 2; }
 
 }  // namespace dash

@@ -794,21 +794,20 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
 // column sums over the rows of slice blockIdx.y: the same reads serve both.  Every part but
 // the last keeps the upper bits (truncated, so that no part overflows); what is left is
 // exact.  256 columns per CTA, eight per lane, rows dealt to the warps.
-template <typename T, int PARTS, bool VEC>
+template <typename T, int PARTS, int MODE>
 __global__ void __launch_bounds__(256)
     split_kernel(const T* dz, long long rows, long long outs, long long ld, long long ldp,
                  long long slice, uint16_t* out, float* sums) {
   __shared__ float sb[8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long c = static_cast<long long>(blockIdx.x) * 256 + lane * 8;
-  const int n = static_cast<int>(outs - c < 8 ? outs - c : 8);
+  const int c = static_cast<int>(blockIdx.x) * 256 + lane * 8;
   const long long r0 = blockIdx.y * slice;
   const long long r1 = r0 + slice < rows ? r0 + slice : rows;
   F2 s[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
 #pragma unroll 2
   for (long long r = r0 + w; r < r1; r += 8) {
     F2 v[4];
-    load8<T, VEC>(dz + r * ld + c, n, v);
+    load8<T, MODE>(dz + r * ld, c, static_cast<int>(outs), v);
     uint32_t word[PARTS][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -836,7 +835,7 @@ __global__ void __launch_bounds__(256)
     }
     // ldp is a multiple of 8 that holds every column: whole words past the last column
     // are the row's padding.
-    if (n > 0)
+    if (c < outs)
 #pragma unroll
       for (int q = 0; q < PARTS; ++q)
         *reinterpret_cast<uint4*>(out + (q * rows + r) * ldp + c) =
@@ -1003,10 +1002,10 @@ cudaError_t run_split(const WeightGradArgs& a, uint16_t* out, float* sums, cudaS
   const bool vec = a.outs % 8 == 0 && (reinterpret_cast<uintptr_t>(dz) & 15u) == 0 &&
                    a.lddz * sizeof(T) % 16 == 0;
   if (vec)
-    split_kernel<T, PARTS, true>
+    split_kernel<T, PARTS, ACC_VEC>
         <<<grid, 256, 0, st>>>(dz, a.rows, a.outs, a.lddz, part_ld(a), slice, out, sums);
   else
-    split_kernel<T, PARTS, false>
+    split_kernel<T, PARTS, ACC_ANY>
         <<<grid, 256, 0, st>>>(dz, a.rows, a.outs, a.lddz, part_ld(a), slice, out, sums);
   return cudaGetLastError();
 }

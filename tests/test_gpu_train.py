@@ -290,6 +290,41 @@ def test_norm_of_strided_views(cols, ld, off, dtype):
                                   atol=2e-5 * float(p.float().abs().max()))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("off", range(8))
+@pytest.mark.parametrize("cols,ld", [(5, 7), (250, 259), (513, 513), (1603, 1606), (4101, 4104),
+                                     (12293, 12300)])
+def test_any_alignment(cols, ld, off, dtype):
+    """Rows that start anywhere, of several warps: the same bits as aligned ones from the
+    checkpoint kernels, the same results to rounding from the norm's."""
+    require_gpu()
+    dr = library()
+    rows = 11
+    x, res, dy = (randn((rows, cols), 60 + i, dtype) for i in range(3))
+    wide = -(-cols // 8) * 8
+    ax, ares, ady = (strided(t, wide) for t in (x, res, dy))  # aligned rows
+    ux, ures, udy, out = (strided(t, ld, off) for t in (x, res, dy, torch.zeros_like(x)))
+    q, s = dr.act_compress(ax, "int8")
+    uq, us = dr.act_compress(ux, "int8")
+    assert (q == uq).all() and (s == us).all()
+    dr.act_restore(q, s, cols, "int8", out=out)
+    assert (out == dr.act_restore(q, s, cols, "int8", dtype)).all() and gaps_untouched(out)
+    r = ures  # in place
+    f = dr.layer_norm_forward(ux, residual=ures, r=r, y=out)
+    assert (r == x + res).all() and gaps_untouched(r) and gaps_untouched(out)
+    want = torch.nn.functional.layer_norm((x + res).double(), (cols,), None, None, 1e-5)
+    d = (out.double() - want).abs()
+    assert (d <= HALF_ULP[dtype] * want.abs() + 1e-5).all()
+    dr.layer_norm_backward(udy, f.rstd, q=q, scale=s, fmt="int8", dx=udy)  # in place
+    n = dr.act_restore(q, s, cols, "int8", torch.float32).double()
+    g = dy.double()
+    m1, m2 = g.mean(1, keepdim=True), (g * n).mean(1, keepdim=True)
+    want = f.rstd.double()[:, None] * (g - m1 - n * m2)
+    d = (udy.double() - want).abs()
+    assert (d <= HALF_ULP[dtype] * want.abs() + 2e-5 * want.abs().max()).all()
+    assert gaps_untouched(udy)
+
+
 def test_constant_and_non_finite_rows():
     require_gpu()
     dr = library()
