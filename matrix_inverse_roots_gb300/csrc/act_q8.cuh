@@ -219,6 +219,14 @@ __device__ __forceinline__ void load8_vec(const T* p, int n, F2 (&v)[4]) {
     v[3] = unpack2<T>(a.w);
   }
 }
+// The eight 16-bit elements in a.
+template <typename T>
+__device__ __forceinline__ void expand8(uint4 a, F2 (&v)[4]) {
+  v[0] = unpack2<T>(a.x);
+  v[1] = unpack2<T>(a.y);
+  v[2] = unpack2<T>(a.z);
+  v[3] = unpack2<T>(a.w);
+}
 template <typename T>
 __device__ __forceinline__ void store8_vec(T* p, int n, const F2 (&v)[4]) {
   if (n <= 0) return;

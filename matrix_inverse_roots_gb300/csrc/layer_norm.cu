@@ -313,9 +313,10 @@ static int bwd_ctas(long long rows) {
 // warps' threads that have columns, where few rows are spread over a CTA's threads.  And a
 // figure for what a thread reaches, taken from such times as these, in us:
 //                                      J = 4             2             1
-//   8192 x 2048 bf16, int8, dres       44.6 (S = 2)  36.5 (S = 5)  42.2 (S = 8)
-//   32768 x 768 bf16, int8, dres       74.6 (S = 3)  58.8 (S = 6)  54.4 (S = 8)
+//   8192 x 2048 bf16, int8, dres       44.6 (S = 2)  36.3 (S = 5)  42.2 (S = 8)
+//   32768 x 768 bf16, int8, dres       74.6 (S = 3)  58.8 (S = 6)  52.7 (S = 8)
 //   8192 x 4096 fp32, int8, dres        159 (S = 0)  88.2 (S = 2)  91.5 (S = 5, G = 1)
+//   8192 x 5632 bf16, from x           80.2 (S = 4)  91.2 (S = 8, G = 1)
 //   16384 x 8192 bf16, e4m3             161 (S = 3)   167 (S = 7, G = 1)
 //   13696 x 1603 bf16, e4m3             107 (S = 0)  86.0 (S = 0)   107 (S = 0)
 // One row at once (G = 1) leaves all warps waiting at its barrier.  The ring pays where
@@ -347,8 +348,8 @@ static BwdPlan bwd_plan(const NormBwdArgs& a) {
     if (!vec || stage < 1024 || each < 2 * p.G || (!p.gamma_fits && J == 1) || fit < 2) fit = 0;
     p.S = static_cast<int>(fit < RING_MAX ? fit : RING_MAX);
     p.stage = static_cast<uint32_t>(stage);
-    double reach = J == 1 ? 0.84 : 1.0;
-    reach *= fit > 3 ? 1.0 : (fit == 3 ? 0.9 : (fit == 2 ? 0.85 : (J == 4 ? 0.4 : 0.55)));
+    double reach = J == 1 ? 0.84 : (J == 2 ? 1.0 : 0.95);
+    reach *= fit > 3 ? 1.0 : (fit == 3 ? 0.95 : (fit == 2 ? 0.85 : (J == 4 ? 0.4 : 0.55)));
     if (p.G == 1 && each > 1) reach *= 0.9;
     const double score = static_cast<double>(nvec) * p.G / (BWD_WARPS * 32 * J) * reach;
     if (score > top) {

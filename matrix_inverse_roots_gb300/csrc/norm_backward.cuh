@@ -69,8 +69,10 @@ enum NSource : int { N_FROM_X = 0, N_INT8 = 1, N_E4M3 = 2 };
 // dgamma = sum dy n and dbeta = sum dy.  Persistent, one CTA per SM: each group takes a row
 // at a time, and a thread keeps its columns from row to row, so that their sums stay in
 // registers and leave once, joined over the groups, as row blockIdx.x of `part`.
-// A row is read twice, before and after its sums.  (Held in registers in between it was
-// slower, 51.6 against 46.8 us at 8192 x 2048: the registers the sums leave are few.)
+// A row is read twice, before and after its sums.  KEEP holds it in registers in between,
+// in 16 bits and codes as it came, where J <= 2 leaves the registers for it: 36.3 against
+// 37.8 us at 8192 x 2048 bf16 with int8 codes and dres; with J = 4 they spill, 239 against
+// 161 us at 16384 x 8192.
 // GS: gamma lies in shared memory, in fp32.  Else it is read from where it is: by short or
 // few rows, and by wide ones whose ring needs the room (4096 x 16384 bf16 with dres: 144
 // us; with gamma's copy and no ring 231).
@@ -87,6 +89,7 @@ template <typename T, int SRC, int J, int MODE, bool RING, bool GS>
 __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     norm_backward_kernel(const NormBwdArgs a, const RowPlan p, float* part) {
   constexpr bool CK = SRC != N_FROM_X;
+  constexpr bool KEEP = RING && sizeof(T) == 2 && J <= 2;
   __shared__ float red[BWD_WARPS][2][2 * 32];
   __shared__ int abort_s;
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -168,16 +171,34 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
                        : static_cast<const T*>(a.x) + (CK ? 0 : r * a.ldx);
     const uint8_t* qp = RING ? st + bytes : a.q + (CK ? r * pitch : 0);
     const F2 rs = f2(rstd), less = f2(-mean);
-    // Vector j: dy and n.
-    auto vector8 = [&](int j, F2 (&d)[4], F2 (&m)[4]) {
+    // Vector j: dy and n.  KEEP: as it was read, for the second time.
+    uint4 kd[KEEP ? J : 1];
+    uint2 kq[KEEP && CK ? J : 1];
+    uint4 kx[KEEP && !CK ? J : 1];
+    auto vector8 = [&](int j, bool again, F2 (&d)[4], F2 (&m)[4]) {
       const int c = c0 + j * cstep;
-      load8<T, MODE>(dyp, c, a.cols, d);
+      if constexpr (KEEP) {
+        if (!again) kd[j] = *reinterpret_cast<const uint4*>(dyp + c);
+        expand8<T>(kd[j], d);
+      } else {
+        load8<T, MODE>(dyp, c, a.cols, d);
+      }
       if constexpr (CK) {
         uint2 q = make_uint2(0u, 0u);
-        if (MODE != ACC_ANY || c < pitch) q = *reinterpret_cast<const uint2*>(qp + c);
+        if constexpr (KEEP) {
+          if (!again) kq[j] = *reinterpret_cast<const uint2*>(qp + c);
+          q = kq[j];
+        } else if (MODE != ACC_ANY || c < pitch) {
+          q = *reinterpret_cast<const uint2*>(qp + c);
+        }
         q8_decode8<SRC == N_INT8 ? DASH_Q8_INT8 : DASH_Q8_E4M3>(q, sc[j], m);
       } else {
-        load8<T, MODE>(xp, c, a.cols, m);
+        if constexpr (KEEP) {
+          if (!again) kx[j] = *reinterpret_cast<const uint4*>(xp + c);
+          expand8<T>(kx[j], m);
+        } else {
+          load8<T, MODE>(xp, c, a.cols, m);
+        }
         // The difference first: x may lie far from zero.
 #pragma unroll
         for (int k = 0; k < 4; ++k) m[k] = (m[k] + less) * rs;
@@ -203,7 +224,7 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     for (int j = 0; j < J; ++j) {
       if (MODE == ACC_VEC && left(j) <= 0) continue;
       F2 gj[4], nj[4];
-      vector8(j, gj, nj);
+      vector8(j, false, gj, nj);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         dg[j][k] = f2_fma(gj[k], nj[k], dg[j][k]);
@@ -233,7 +254,7 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     for (int j = 0; j < J; ++j) {
       if (MODE == ACC_VEC && left(j) <= 0) continue;
       F2 gj[4], nj[4], rj[4];
-      vector8(j, gj, nj);
+      vector8(j, true, gj, nj);
       scale8(j, gj);
 #pragma unroll
       for (int k = 0; k < 4; ++k) gj[k] = f2_fma(nj[k], m2, gj[k] + m1) * rs;
