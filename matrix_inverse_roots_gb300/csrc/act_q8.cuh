@@ -104,10 +104,9 @@ __device__ __forceinline__ float q8_value(uint32_t code) {
 
 // ---------------------------------------------------------------- packed fp32 pairs
 // Two fp32 numbers in one 64-bit register, each operation on both in one instruction with
-// the rounding of the single one.  The norm and checkpoint kernels issue some ten
-// instructions per element with these and twice that without, and issue is what holds
-// them below HBM's rate for 16-bit types.
-
+// the rounding of the single one.  The norm kernels issue some 30 instructions per element
+// with these, most of them conversions, packing and addresses, and the issue slots they
+// leave are few for 16-bit types (half of them are used at 8192 x 2048).
 struct F2 {
   uint64_t v;
 };

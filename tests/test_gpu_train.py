@@ -574,6 +574,27 @@ def test_weight_grad_over_many_tiles_every_run(rows, outs, cols, dtype, odt, fmt
     assert dr.device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("exp", [-126, -118, -90, 90, 118, 126])
+def test_weight_grad_at_the_ends_of_the_scale(exp, fmt):
+    """Checkpoints whose values lie at either end of fp32's range (below, some are bf16
+    subnormals), with dz at the other end, so that the sums are ordinary numbers."""
+    require_gpu()
+    dr = library()
+    rows, outs, cols = 200, 130, 300
+    x = torch.ldexp(randn((rows, cols), 62).clamp(-1.9, 1.9),
+                    torch.tensor(float(exp), device="cuda"))
+    q, s = dr.act_compress(x, fmt)
+    n = t64.restore(q.cpu().numpy(), s.cpu().numpy(), cols, fmt)
+    dz = torch.ldexp(randn((rows, outs), 63, torch.bfloat16).clamp(-1.9, 1.9),
+                     torch.tensor(float(-exp), device="cuda", dtype=torch.bfloat16))
+    for odt in (torch.float32, torch.bfloat16):
+        dw0, _, e, _ = wg_bound(to64(dz), n, None, None, 1)
+        dw, _ = dr.weight_grad(dz, q, s, cols, fmt, dtype=odt)
+        check(dw, dw0, rounded(dw0, e, odt), "dW")
+    assert dr.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_weight_grad_of_strided_views(dtype):
     require_gpu()
