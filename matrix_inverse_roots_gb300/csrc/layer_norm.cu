@@ -177,8 +177,15 @@ __global__ void __launch_bounds__(32 * PS_WARPS)
   const float* p0 = part + blockIdx.y * cols + c;
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 8
-    for (int p = w; p < parts; p += PS_WARPS) s += p0[p * stride];
+    // Ten loads at once: the parts of one persistent kernel.
+    for (int p = w; p < parts; p += 10 * PS_WARPS) {
+      float v[10];
+#pragma unroll
+      for (int k = 0; k < 10; ++k)
+        v[k] = p + k * PS_WARPS < parts ? p0[(p + k * PS_WARPS) * stride] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 10; ++k) s += v[k];
+    }
   }
   sm[w][lane] = s;
   __syncthreads();
@@ -313,12 +320,12 @@ static int bwd_ctas(long long rows) {
 // warps' threads that have columns, where few rows are spread over a CTA's threads.  And a
 // figure for what a thread reaches, taken from such times as these, in us:
 //                                      J = 4             2             1
-//   8192 x 2048 bf16, int8, dres       44.6 (S = 2)  36.3 (S = 5)  42.2 (S = 8)
-//   32768 x 768 bf16, int8, dres       74.6 (S = 3)  58.8 (S = 6)  52.7 (S = 8)
-//   8192 x 4096 fp32, int8, dres        159 (S = 0)  88.2 (S = 2)  91.5 (S = 5, G = 1)
-//   8192 x 5632 bf16, from x           80.2 (S = 4)  91.2 (S = 8, G = 1)
-//   16384 x 8192 bf16, e4m3             161 (S = 3)   167 (S = 7, G = 1)
-//   13696 x 1603 bf16, e4m3             107 (S = 0)  86.0 (S = 0)   107 (S = 0)
+//   8192 x 2048 bf16, int8, dres       33.0 (S = 2)  30.6 (S = 5)  37.6 (S = 8)
+//   32768 x 768 bf16, int8, dres       56.5 (S = 3)  54.7 (S = 6)  50.4 (S = 8)
+//   8192 x 4096 fp32, int8, dres        138 (S = 0)  82.7 (S = 2)  83.5 (S = 5, G = 1)
+//   8192 x 5632 bf16, from x           71.1 (S = 4)  77.3 (S = 8, G = 1)
+//   16384 x 8192 bf16, e4m3             131 (S = 3)   147 (S = 7, G = 1)
+//   13696 x 1603 bf16, e4m3            82.9 (S = 0)  81.5 (S = 0)   103 (S = 0)
 // One row at once (G = 1) leaves all warps waiting at its barrier.  The ring pays where
 // every group has several rows of a KB or more, and needs two stages; gamma's copy makes
 // way where only without it two fit (J = 1, narrow rows, has the room).
@@ -327,8 +334,7 @@ static BwdPlan bwd_plan(const NormBwdArgs& a) {
   double top = -1.0;
   const int nvec = a.cols > 0 ? (a.cols + 7) / 8 : 1;
   const size_t row = static_cast<size_t>(a.cols) * dt_bytes(a.dt);
-  const size_t stage = row * (a.dres ? 2 : 1) +
-                       (a.q ? (a.cols + Q8_GROUP - 1) / Q8_GROUP * Q8_GROUP : row);
+  const int ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP;
   const bool vec = a.cols % 8 == 0 && vec_ok(a.dy, a.lddy, a.dt) && vec_ok(a.dx, a.lddx, a.dt) &&
                    (!a.x || vec_ok(a.x, a.ldx, a.dt)) &&
                    (!a.dres || vec_ok(a.dres, a.lddres, a.dt));
@@ -342,6 +348,10 @@ static BwdPlan bwd_plan(const NormBwdArgs& a) {
     p.G = BWD_WARPS / p.W;
     if (p.G > each) p.G = static_cast<int>(each);
     p.vec = vec;
+    p.sring = a.q && J > 1 && ng % 16 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15u) == 0;
+    p.full = vec && a.cols == 256 * p.W * J && (!a.q || J == 1 || p.sring);
+    const size_t stage =
+        row * (a.dres ? 2 : 1) + (a.q ? ng * Q8_GROUP : row) + (p.sring ? ng : 0);
     const size_t room = BWD_SMEM - RING_BARS, stages = stage * p.G;
     p.gamma_fits = 2 * stages + gamma_room(a.cols) <= room;
     size_t fit = (p.gamma_fits ? room - gamma_room(a.cols) : room) / stages;

@@ -10,35 +10,36 @@
 namespace dash {
 
 // Joins the groups' column sums, in order, into row blockIdx.x of `part` (dgamma's sums,
-// then dbeta's).  sums: 2 cols floats of shared memory.
+// then dbeta's).  sums: 2 x cols floats of shared memory, cols to a multiple of eight.
 template <int J>
 __device__ __forceinline__ void join_groups(float* sums, float* part, int cols, int W, int G,
-                                            int grp, int t, const F2 (&dg)[J][4],
+                                            int grp, int t, bool has_db, const F2 (&dg)[J][4],
                                             const F2 (&db)[J][4]) {
   float* out = part + static_cast<long long>(blockIdx.x) * 2 * cols;
+  const int pc = (cols + 7) / 8 * 8;
+  auto one = [&](const F2 (&v)[4], float* sm, float* to, int i, int n) {
+    F2 r[4] = {v[0], v[1], v[2], v[3]};
+    if (i > 0) {
+      F2 w[4];
+      load8_vec<float>(sm, 8, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = r[k] + w[k];
+    }
+    if (i + 1 < G)
+      store8_vec<float>(sm, 8, r);
+    else if (cols % 8 == 0)
+      store8_vec<float>(to, 8, r);
+    else
+      store8_any<float>(to, n, r);
+  };
   for (int i = 0; i < G; ++i) {
     if (grp == i) {
-      float* to = i + 1 < G ? sums : out;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int c = (j * 32 * W + t) * 8;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float g[2], b[2];
-          f2_get(dg[j][k], g[0], g[1]);
-          f2_get(db[j][k], b[0], b[1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = c + 2 * k + h;
-            if (col >= cols) continue;
-            if (i > 0) {
-              g[h] += sums[col];
-              b[h] += sums[cols + col];
-            }
-            to[col] = g[h];
-            to[cols + col] = b[h];
-          }
-        }
+        if (c >= cols) continue;
+        one(dg[j], sums + c, out + c, i, cols - c);
+        if (has_db) one(db[j], sums + pc + c, out + cols + c, i, cols - c);
       }
     }
     if (i + 1 < G) __syncthreads();
@@ -56,11 +57,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // W warps per row, G groups of them per CTA; with the ring, S stages of `stage` bytes for
 // each group.  goff: the offset of gamma's copy in dynamic shared memory; gvec: gamma
-// itself lies at a 16-byte boundary.
+// itself lies at a 16-byte boundary; sring: a stage holds the scales too.
 struct RowPlan {
   int W, G, S;
   uint32_t stage, goff;
-  bool gvec;
+  bool gvec, sring;
 };
 
 // Where n comes from.
@@ -104,22 +105,20 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     for (int i = 0; i < p.G * p.S; ++i) mbar_init(smem_u32(dyn) + 8u * i, 1);
     fence_barrier_init();
   }
-  if (GS)
-    for (int c = threadIdx.x; c < (a.cols + 7) / 8 * 8; c += blockDim.x)
-      gs[c] = a.gamma && c < a.cols ? load_dt(a.gamma, a.wdt, c) : 1.0f;
-  __syncthreads();
   const int rows = static_cast<int>(a.rows);
   const uint32_t step = gridDim.x * p.G, row0 = blockIdx.x * p.G + grp;
   const int ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP, pitch = ng * Q8_GROUP;
+  // Scales in the ring.  (ACC_FULL rows have whole 16-byte words of them.)
+  const bool sr = RING && CK && J > 1 && (MODE == ACC_FULL || p.sring);
   const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
   const uint32_t nbytes = CK ? static_cast<uint32_t>(pitch) : bytes;
-  // A stage: dy, x or the codes, dres.
+  // A stage: dy, x or the codes, dres, the scales.
   auto fill = [&](uint32_t row, int s) {
     if (row >= static_cast<uint32_t>(rows) || *abort_flag) return;
     const long long r = row;
     const uint32_t bar = bars + 8u * s;
     const uint32_t dst = data + (grp * p.S + s) * p.stage;
-    mbar_arrive_expect_tx(bar, bytes + nbytes + (a.dres ? bytes : 0u));
+    mbar_arrive_expect_tx(bar, bytes + nbytes + (a.dres ? bytes : 0u) + (sr ? ng : 0));
     bulk_load(dst, static_cast<const T*>(a.dy) + r * a.lddy, bytes, bar);
     if (CK)
       bulk_load(dst + bytes, a.q + r * pitch, nbytes, bar);
@@ -127,7 +126,9 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
       bulk_load(dst + bytes, static_cast<const T*>(a.x) + r * a.ldx, nbytes, bar);
     if (a.dres)
       bulk_load(dst + bytes + nbytes, static_cast<const T*>(a.dres) + r * a.lddres, bytes, bar);
+    if (sr) bulk_load(dst + p.stage - ng, a.scale + r * ng, ng, bar);
   };
+  if (RING) __syncthreads();  // the barriers exist
   if (RING && first)
     for (int s = 0; s < p.S; ++s) fill(row0 + s * step, s);
   const int c0 = t * 8, cstep = 256 * W;  // columns c0 + j cstep
@@ -138,7 +139,9 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) dg[j][k] = db[j][k] = f2(0.0f);
-  // Scales and statistics come straight from global memory, one row ahead.
+  // Statistics come straight from global memory, one row ahead, and so do scales that are
+  // not in the ring (a few bytes per load, whose waits others share: 161 against 131
+  // us at 16384 x 8192 with e4m3 codes).
   constexpr int NSC = CK ? J : 1;
   uint32_t sc[NSC] = {};
   float rstd = 0.0f, mean = 0.0f;
@@ -147,13 +150,21 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
       const uint8_t* sp = a.scale + static_cast<long long>(row) * ng + t / 4;
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        b[j] = MODE == ACC_FULL || c0 + j * cstep < pitch ? sp[j * (cstep / 32)] : 127u;
+        if (!sr)
+          b[j] = MODE == ACC_FULL || c0 + j * cstep < pitch ? sp[j * (cstep / 32)] : 127u;
     } else if (a.center) {
       mu = a.mean[row];
     }
     rs = a.rstd[row];
   };
   if (row0 < static_cast<uint32_t>(rows)) small(row0, sc, rstd, mean);
+  if (GS)
+    for (int c = threadIdx.x * 8; c < a.cols; c += blockDim.x * 8) {
+      F2 w[4] = {f2(1.0f), f2(1.0f), f2(1.0f), f2(1.0f)};
+      if (a.gamma) load8_dt(a.gamma, a.wdt, p.gvec, c, a.cols - c, w);
+      store8_vec<float>(gs + c, 8, w);
+    }
+  __syncthreads();
   const float inv = 1.0f / a.cols;
   const bool has_db = a.dbeta != nullptr;
   int s = 0, flip = 0;
@@ -170,6 +181,11 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     const T* xp = RING ? reinterpret_cast<const T*>(st + bytes)
                        : static_cast<const T*>(a.x) + (CK ? 0 : r * a.ldx);
     const uint8_t* qp = RING ? st + bytes : a.q + (CK ? r * pitch : 0);
+    if (sr)
+#pragma unroll
+      for (int j = 0; j < NSC; ++j)
+        if (MODE == ACC_FULL || c0 + j * cstep < pitch)
+          sc[j] = st[p.stage - ng + t / 4 + j * (cstep / 32)];
     const F2 rs = f2(rstd), less = f2(-mean);
     // Vector j: dy and n.  KEEP: as it was read, for the second time.
     uint4 kd[KEEP ? J : 1];
@@ -270,14 +286,15 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
       ph ^= 1u;
     }
 #pragma unroll
-    for (int j = 0; j < NSC; ++j) sc[j] = nsc[j];
+    for (int j = 0; j < NSC; ++j)
+      if (!sr) sc[j] = nsc[j];
     rstd = nrstd;
     mean = nmean;
   }
   if (part == nullptr) return;
   // Every copy has landed and been read, and gamma too: the groups' sums take their place.
   __syncthreads();
-  join_groups<J>(reinterpret_cast<float*>(dyn), part, a.cols, W, p.G, grp, t, dg, db);
+  join_groups<J>(reinterpret_cast<float*>(dyn), part, a.cols, W, p.G, grp, t, has_db, dg, db);
 }
 
 // ---------------------------------------------------------------- host side
@@ -289,7 +306,7 @@ dash_status backward_k(const NormBwdArgs& a, const BwdPlan& b, RowPlan p, float*
   p.goff = RING ? static_cast<uint32_t>(p.G) * p.S * p.stage + RING_BARS : 0;
   p.gvec = (reinterpret_cast<uintptr_t>(a.gamma) & 15u) == 0;
   size_t smem = p.goff + (GS ? gamma_room(a.cols) : 0);
-  const size_t join = part && p.G > 1 ? static_cast<size_t>(a.cols) * 8 : 0;
+  const size_t join = part && p.G > 1 ? gamma_room(a.cols) * 2 : 0;
   if (smem < join) smem = join;
   if (smem > 32 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)) != cudaSuccess)
@@ -300,10 +317,10 @@ dash_status backward_k(const NormBwdArgs& a, const BwdPlan& b, RowPlan p, float*
 
 template <typename T, int SRC, int J>
 dash_status backward_j(const NormBwdArgs& a, const BwdPlan& b, float* part, cudaStream_t st) {
-  RowPlan p = {b.W, b.G, b.S, b.stage, 0, false};
+  RowPlan p = {b.W, b.G, b.S, b.stage, 0, false, b.sring};
   if (!b.vec) return backward_k<T, SRC, J, ACC_ANY, false, true>(a, b, p, part, st);
   if (b.S == 0) return backward_k<T, SRC, J, ACC_VEC, false, false>(a, b, p, part, st);
-  const bool full = a.cols == 256 * b.W * J;
+  const bool full = b.full;
   if constexpr (J > 1) {
     if (!b.gamma_fits)
       return full ? backward_k<T, SRC, J, ACC_FULL, true, false>(a, b, p, part, st)

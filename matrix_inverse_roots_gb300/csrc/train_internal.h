@@ -85,11 +85,12 @@ struct NormBwdArgs {
 };
 // How a backward pass is laid out: J vectors per thread, W warps per row, G rows at once
 // per CTA, one persistent CTA per SM; a ring of S stages per row at once (0: none), of
-// `stage` bytes; whether gamma's copy fits beside it, and 16-byte accesses the rows.
+// `stage` bytes, with the scales (sring) where they are whole 16-byte words; whether gamma's
+// copy fits beside it, 16-byte accesses fit the rows, and the rows fill their warps exactly.
 struct BwdPlan {
   int J, W, G, S, grid;
   uint32_t stage;
-  bool gamma_fits, vec;
+  bool sring, gamma_fits, vec, full;
 };
 constexpr int BWD_WARPS = 16;                        // of a backward CTA, at most
 constexpr int RING_MAX = 8;                          // most stages of a group
