@@ -4,6 +4,8 @@
 // (four neighbouring lanes share a group, so its largest magnitude takes two shuffles) and
 // issues all their loads before the first use: Q8_U of them, 16 to 32 KB of reads in
 // flight per 256 threads.
+#include <type_traits>
+
 #include "act_q8.cuh"
 #include "dash_internal.h"
 #include "train_internal.h"
@@ -12,84 +14,6 @@ namespace dash {
 
 constexpr int Q8_THREADS = 256;
 constexpr int Q8_U = 4;
-
-// out = the N words that start `bytes` (0 .. 15) into the words w (N + 4 of them).
-template <int N>
-__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], uint32_t bytes,
-                                            uint32_t (&out)[N]) {
-  if (bytes & 8u) {
-#pragma unroll
-    for (int k = 0; k < N + 2; ++k) w[k] = w[k + 2];
-  }
-  if (bytes & 4u) {
-#pragma unroll
-    for (int k = 0; k < N + 1; ++k) w[k] = w[k + 1];
-  }
-  const uint32_t r = (bytes & 3u) * 8u;
-#pragma unroll
-  for (int k = 0; k < N; ++k) out[k] = __funnelshift_r(w[k], w[k + 1], r);
-}
-
-// Eight elements to columns c .. c + 7 of a row at any address; lane l of the warp has
-// columns c0 + 8 l, and the whole warp calls.  A lane stores the aligned 16-byte words that
-// begin in its elements, with the next lane's first bytes; what a warp or a row begins or
-// ends with goes singly.  (All of it singly: 63 against 31 us for act_restore of
-// 13696 x 1603 bf16.)
-template <typename T>
-__device__ __forceinline__ void store8_joined(T* row, int c, int cols, const F2 (&v)[4]) {
-  constexpr int N = static_cast<int>(sizeof(T)) * 2;
-  constexpr int B = 8 * static_cast<int>(sizeof(T));
-  const uintptr_t r1 = reinterpret_cast<uintptr_t>(row) + cols * sizeof(T);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + static_cast<uintptr_t>(c) * sizeof(T);
-  const uint32_t off = static_cast<uint32_t>(at & 15u);
-  uint32_t w[N + 4], out[N];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if constexpr (sizeof(T) == 4) {
-      float lo, hi;
-      f2_get(v[k], lo, hi);
-      w[2 * k] = __float_as_uint(lo);
-      w[2 * k + 1] = __float_as_uint(hi);
-    } else {
-      w[k] = pack2<T>(v[k]);
-    }
-  }
-  const int lane = threadIdx.x & 31;
-  const uint32_t head = off ? 16u - off : 0u;  // own bytes before the first boundary
-  const uintptr_t f = at + head;
-  // Whether this lane stores whole words [f, f + B), and whether the lane before does (its
-  // words end at f and hold this lane's head).
-  const bool whole = f + B <= r1 && (off == 0 || lane < 31);
-  const bool covered = off == 0 || (lane > 0 && f <= r1);
-  uint32_t own[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) own[k] = w[k];
-  if (off != 0) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[N + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
-    shift_words<N>(w, head, out);
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) out[k] = w[k];
-  }
-  if (whole)
-#pragma unroll
-    for (int k = 0; k < N; k += 4)
-      *reinterpret_cast<uint4*>(f + 4 * k) = make_uint4(out[k], out[k + 1], out[k + 2], out[k + 3]);
-  if (!whole || !covered) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uintptr_t e = at + k * sizeof(T);
-      if (e < r1 && (e < f ? !covered : !whole)) {
-        if constexpr (sizeof(T) == 4)
-          *reinterpret_cast<uint32_t*>(e) = own[k];
-        else
-          *reinterpret_cast<uint16_t*>(e) =
-              static_cast<uint16_t>(own[k / 2] >> (16 * (k & 1)));
-      }
-    }
-  }
-}
 
 // Vector i of the padded matrix, nv vectors a row.  FLAT (rows of whole groups, without
 // gaps): i alone addresses it.  Else its row and column come from a 32-bit division within
@@ -102,18 +26,31 @@ __global__ void __launch_bounds__(Q8_THREADS)
   const unsigned v0 = FLAT ? 0 : static_cast<unsigned>(base - row0 * nv);
   const T* x = static_cast<const T*>(a.x);
   F2 v[Q8_U][4];
+  // Whether all rows of the tile are inner ones.
+  const bool inner = MODE == ACC_ANY && inner_row<T>(row0, a.rows, a.cols) &&
+                     row0 + (v0 + Q8_THREADS * Q8_U - 1) / nv < a.rows - 1;
+  auto load = [&](auto in) {
 #pragma unroll
-  for (int u = 0; u < Q8_U; ++u) {
-    const unsigned off = u * Q8_THREADS + threadIdx.x;
-    const long long i = base + off;
-    if (FLAT) {
-      load8_vec<T>(x + i * 8, i < total ? 8 : 0, v[u]);
-    } else {
-      const unsigned k = (v0 + off) / nv;
-      const int c = static_cast<int>(v0 + off - k * nv) * 8;
-      load8<T, MODE>(x + (row0 + k) * a.ld, c, i < total ? static_cast<int>(a.cols) : c, v[u]);
+    for (int u = 0; u < Q8_U; ++u) {
+      const unsigned off = u * Q8_THREADS + threadIdx.x;
+      const long long i = base + off;
+      if (FLAT) {
+        load8_vec<T>(x + i * 8, i < total ? 8 : 0, v[u]);
+      } else {
+        const unsigned k = (v0 + off) / nv;
+        const int c = static_cast<int>(v0 + off - k * nv) * 8;
+        const T* row = x + (row0 + k) * a.ld;
+        if constexpr (decltype(in)::value)
+          load8_inner<T>(row + c, static_cast<int>(a.cols) - c, v[u]);
+        else
+          load8<T, MODE>(row, c, i < total ? static_cast<int>(a.cols) : c, v[u]);
+      }
     }
-  }
+  };
+  if (inner)
+    load(std::true_type());
+  else
+    load(std::false_type());
 #pragma unroll
   for (int u = 0; u < Q8_U; ++u) {
     const long long i = base + u * Q8_THREADS + threadIdx.x;
@@ -174,10 +111,7 @@ __global__ void __launch_bounds__(Q8_THREADS)
     } else if (in[u]) {  // the same for the whole warp
       T* to = x + row[u] * a.ld;
       const int c = static_cast<int>(col[u]), cols = static_cast<int>(a.cols);
-      if constexpr (MODE == ACC_ANY)
-        store8_joined<T>(to, c, cols, v);
-      else
-        store8_vec<T>(to + c, cols - c, v);
+      store8<T, MODE>(to, c, cols, v);
     }
   }
 }

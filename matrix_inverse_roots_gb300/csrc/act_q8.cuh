@@ -176,26 +176,13 @@ __device__ __forceinline__ uint32_t pack2(F2 a) {
 enum Access : int { ACC_ANY = 0, ACC_VEC = 1, ACC_FULL = 2 };  // FULL: all exist
 
 // Eight elements from p at any address, of which n exist; the others are zero.  (Read
-// singly: L1 serves a warp's 512 bytes to its eight loads.  Aligned 16-byte loads whose
-// words are shifted and joined across lanes took longer: 33 against 20 us for act_compress
-// of 13696 x 1603 bf16, 116 against 87 us for the norm's backward pass.)
+// singly; the first and last rows of a matrix, and short ones.)
 template <typename T>
 __device__ __forceinline__ void load8_any(const T* p, int n, F2 (&v)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     v[k] = f2(2 * k < n ? Elem<T>::to(p[2 * k]) : 0.0f,
               2 * k + 1 < n ? Elem<T>::to(p[2 * k + 1]) : 0.0f);
-}
-
-template <typename T>
-__device__ __forceinline__ void store8_any(T* p, int n, const F2 (&v)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float lo, hi;
-    f2_get(v[k], lo, hi);
-    if (2 * k < n) p[2 * k] = Elem<T>::from(lo);
-    if (2 * k + 1 < n) p[2 * k + 1] = Elem<T>::from(hi);
-  }
 }
 
 // Eight elements from p, at a 16-byte boundary; zeros unless n > 0.
@@ -241,7 +228,166 @@ __device__ __forceinline__ void store8_vec(T* p, int n, const F2 (&v)[4]) {
   }
 }
 
-// Columns c .. c + 7 of a row, either way.
+// out = the N words that start `bytes` (0 .. 15) into the words w (N + 4 of them).
+template <int N>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[N + 4], uint32_t bytes,
+                                            uint32_t (&out)[N]) {
+  if (bytes & 8u) {
+#pragma unroll
+    for (int k = 0; k < N + 2; ++k) w[k] = w[k + 2];
+  }
+  if (bytes & 4u) {
+#pragma unroll
+    for (int k = 0; k < N + 1; ++k) w[k] = w[k + 1];
+  }
+  const uint32_t r = (bytes & 3u) * 8u;
+#pragma unroll
+  for (int k = 0; k < N; ++k) out[k] = __funnelshift_r(w[k], w[k + 1], r);
+}
+
+// Words of eight elements, and of the 16-byte words that hold them at any address.
+template <typename T>
+constexpr int WORDS = static_cast<int>(sizeof(T)) * 2;
+
+// The words of n elements (1 .. 8) that start `off` bytes into w; what follows them is zero.
+template <typename T>
+__device__ __forceinline__ void cut8(uint32_t (&w)[WORDS<T> + 4], uint32_t off, int n,
+                                     uint32_t (&out)[WORDS<T>]) {
+  shift_words<WORDS<T>>(w, off, out);
+  if (n < 8) {
+#pragma unroll
+    for (int k = 0; k < WORDS<T>; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        if (k >= n) out[k] = 0u;
+      } else {
+        if (2 * k >= n)
+          out[k] = 0u;
+        else if (2 * k + 1 >= n)
+          out[k] &= 0xffffu;
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void words8(const uint32_t (&w)[WORDS<T>], F2 (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4)
+      v[k] = f2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    else
+      v[k] = unpack2<T>(w[k]);
+  }
+}
+
+// Whether 16-byte words that hold elements of this row lie in its matrix: not of the first
+// and last row, whose words may begin before the matrix or end past it.
+template <typename T>
+__device__ __forceinline__ bool inner_row(long long row, long long rows, long long cols) {
+  return row > 0 && row < rows - 1 && cols * static_cast<int>(sizeof(T)) >= 16;
+}
+
+// Eight elements at any address p in an inner row, of which n exist (any n); the others are
+// zero.  Aligned 16-byte words, two (three of fp32), shifted into place.
+template <typename T>
+__device__ __forceinline__ void load8_inner(const T* p, int n, F2 (&v)[4]) {
+  n = n < 8 ? n : 8;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const int off = static_cast<int>(at & 15u);
+  const uint4* f = reinterpret_cast<const uint4*>(at - off);
+  uint32_t w[WORDS<T> + 4], out[WORDS<T>];
+#pragma unroll
+  for (int k = 0; k < WORDS<T> + 4; k += 4) {
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (n > 0 && 4 * k - off < n * static_cast<int>(sizeof(T))) q = f[k / 4];
+    w[k] = q.x;
+    w[k + 1] = q.y;
+    w[k + 2] = q.z;
+    w[k + 3] = q.w;
+  }
+  cut8<T>(w, off, n, out);
+  words8<T>(out, v);
+}
+
+// The same from shared memory: p is the 16-byte boundary before the elements, off their
+// distance from it.  Reads 16 bytes more than the elements take.
+template <typename T>
+__device__ __forceinline__ void read8_shared(const uint8_t* p, uint32_t off, int n,
+                                             uint32_t (&out)[WORDS<T>]) {
+  uint32_t w[WORDS<T> + 4];
+#pragma unroll
+  for (int k = 0; k < WORDS<T> + 4; k += 4) {
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (n > 0) q = reinterpret_cast<const uint4*>(p)[k / 4];
+    w[k] = q.x;
+    w[k + 1] = q.y;
+    w[k + 2] = q.z;
+    w[k + 3] = q.w;
+  }
+  cut8<T>(w, off, n, out);
+}
+
+// Eight elements to columns c .. c + 7 of a row at any address; lane l of the warp has
+// columns c0 + 8 l, and the whole warp calls.  A lane stores the aligned 16-byte words that
+// begin in its elements, with the next lane's first bytes; what a warp or a row begins or
+// ends with goes singly.  (All of it singly: 63 against 31 us for act_restore of
+// 13696 x 1603 bf16.)
+template <typename T>
+__device__ __forceinline__ void store8_joined(T* row, int c, int cols, const F2 (&v)[4]) {
+  constexpr int N = static_cast<int>(sizeof(T)) * 2;
+  constexpr int B = 8 * static_cast<int>(sizeof(T));
+  const uintptr_t r1 = reinterpret_cast<uintptr_t>(row) + cols * sizeof(T);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + static_cast<uintptr_t>(c) * sizeof(T);
+  const uint32_t off = static_cast<uint32_t>(at & 15u);
+  uint32_t w[N + 4], out[N];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      float lo, hi;
+      f2_get(v[k], lo, hi);
+      w[2 * k] = __float_as_uint(lo);
+      w[2 * k + 1] = __float_as_uint(hi);
+    } else {
+      w[k] = pack2<T>(v[k]);
+    }
+  }
+  const int lane = threadIdx.x & 31;
+  const uint32_t head = off ? 16u - off : 0u;  // own bytes before the first boundary
+  const uintptr_t f = at + head;
+  // Whether this lane stores whole words [f, f + B), and whether the lane before does (its
+  // words end at f and hold this lane's head).
+  const bool whole = f + B <= r1 && (off == 0 || lane < 31);
+  const bool covered = off == 0 || (lane > 0 && f <= r1);
+  uint32_t own[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) own[k] = w[k];
+  if (off != 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[N + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
+    shift_words<N>(w, head, out);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) out[k] = w[k];
+  }
+  if (whole)
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+      *reinterpret_cast<uint4*>(f + 4 * k) = make_uint4(out[k], out[k + 1], out[k + 2], out[k + 3]);
+  if (!whole || !covered) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uintptr_t e = at + k * sizeof(T);
+      if (e < r1 && (e < f ? !covered : !whole)) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<uint32_t*>(e) = own[k];
+        else
+          *reinterpret_cast<uint16_t*>(e) =
+              static_cast<uint16_t>(own[k / 2] >> (16 * (k & 1)));
+      }
+    }
+  }
+}
+
+// Columns c .. c + 7 of a row, either way.  (Storing with ACC_ANY, the whole warp calls.)
 template <typename T, int MODE>
 __device__ __forceinline__ void load8(const T* row, int c, int cols, F2 (&v)[4]) {
   if constexpr (MODE == ACC_ANY)
@@ -252,7 +398,7 @@ __device__ __forceinline__ void load8(const T* row, int c, int cols, F2 (&v)[4])
 template <typename T, int MODE>
 __device__ __forceinline__ void store8(T* row, int c, int cols, const F2 (&v)[4]) {
   if constexpr (MODE == ACC_ANY)
-    store8_any<T>(row + c, cols - c, v);
+    store8_joined<T>(row, c, cols, v);
   else
     store8_vec<T>(row + c, MODE == ACC_FULL ? 8 : cols - c, v);
 }

@@ -2,6 +2,8 @@
 // root-mean-square norm), with an optional 8-bit checkpoint of the normalised rows, and
 // column sums.  All of it is bound by HBM, or at a few rows by the latency of one launch:
 // every kernel reads its rows once and keeps them in registers.
+#include <type_traits>
+
 #include "dash_internal.h"
 #include "norm_common.cuh"
 #include "train_internal.h"
@@ -33,19 +35,31 @@ __global__ void __launch_bounds__(fwd_threads(J))
   const int t = W == 1 ? lane : static_cast<int>(threadIdx.x);
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   F2 v[J][4];
+  auto load = [&](auto in) {
+    auto load8_row = [&](const T* p, int c, F2 (&u)[4]) {
+      if constexpr (decltype(in)::value)
+        load8_inner<T>(p + c, a.cols - c, u);
+      else
+        load8<T, MODE>(p, c, a.cols, u);
+    };
 #pragma unroll
-  for (int j = 0; j < J; ++j) load8<T, MODE>(x, (j * 32 * W + t) * 8, a.cols, v[j]);
-  if (a.residual) {
-    // The stream is carried in its own type: the norm sees the rounded sum.
-    const T* res = static_cast<const T*>(a.residual) + row * a.ldres;
+    for (int j = 0; j < J; ++j) load8_row(x, (j * 32 * W + t) * 8, v[j]);
+    if (a.residual) {
+      // The stream is carried in its own type: the norm sees the rounded sum.
+      const T* res = static_cast<const T*>(a.residual) + row * a.ldres;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      F2 u[4];
-      load8<T, MODE>(res, (j * 32 * W + t) * 8, a.cols, u);
+      for (int j = 0; j < J; ++j) {
+        F2 u[4];
+        load8_row(res, (j * 32 * W + t) * 8, u);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[j][k] = round2<T>(v[j][k] + u[k]);
+        for (int k = 0; k < 4; ++k) v[j][k] = round2<T>(v[j][k] + u[k]);
+      }
     }
-  }
+  };
+  if (MODE == ACC_ANY && inner_row<T>(row, a.rows, a.cols))
+    load(std::integral_constant<bool, MODE == ACC_ANY>());
+  else
+    load(std::false_type());
   if (a.r) {
     T* r = static_cast<T*>(a.r) + row * a.ldr;
 #pragma unroll
@@ -108,7 +122,8 @@ __global__ void __launch_bounds__(fwd_threads(J))
       }
     }
     const int n = MODE == ACC_FULL ? 8 : a.cols - c;
-    if (n > 0) {
+    // (With ACC_ANY the whole warp stores.)
+    if (MODE == ACC_ANY || n > 0) {
       F2 w[4];
       if (a.gamma) {
         load8_dt(a.gamma, a.wdt, wvec, c, n, w);
@@ -350,12 +365,13 @@ static BwdPlan bwd_plan(const NormBwdArgs& a) {
     p.vec = vec;
     p.sring = a.q && J > 1 && ng % 16 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15u) == 0;
     p.full = vec && a.cols == 256 * p.W * J && (!a.q || J == 1 || p.sring);
+    const size_t in = ring_row(row, !vec);
     const size_t stage =
-        row * (a.dres ? 2 : 1) + (a.q ? ng * Q8_GROUP : row) + (p.sring ? ng : 0);
+        in * (a.dres ? 2 : 1) + (a.q ? ng * Q8_GROUP : in) + (p.sring ? ng : 0);
     const size_t room = BWD_SMEM - RING_BARS, stages = stage * p.G;
     p.gamma_fits = 2 * stages + gamma_room(a.cols) <= room;
     size_t fit = (p.gamma_fits ? room - gamma_room(a.cols) : room) / stages;
-    if (!vec || stage < 1024 || each < 2 * p.G || (!p.gamma_fits && J == 1) || fit < 2) fit = 0;
+    if (stage < 1024 || each < 2 * p.G || (!p.gamma_fits && (!vec || J == 1)) || fit < 2) fit = 0;
     p.S = static_cast<int>(fit < RING_MAX ? fit : RING_MAX);
     p.stage = static_cast<uint32_t>(stage);
     double reach = J == 1 ? 0.84 : (J == 2 ? 1.0 : 0.95);

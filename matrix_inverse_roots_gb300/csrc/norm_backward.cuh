@@ -9,6 +9,16 @@
 
 namespace dash {
 
+__device__ __forceinline__ void store_singly(float* p, int n, const F2 (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo, hi;
+    f2_get(v[k], lo, hi);
+    if (2 * k < n) p[2 * k] = lo;
+    if (2 * k + 1 < n) p[2 * k + 1] = hi;
+  }
+}
+
 // Joins the groups' column sums, in order, into row blockIdx.x of `part` (dgamma's sums,
 // then dbeta's).  sums: 2 x cols floats of shared memory, cols to a multiple of eight.
 template <int J>
@@ -30,7 +40,7 @@ __device__ __forceinline__ void join_groups(float* sums, float* part, int cols, 
     else if (cols % 8 == 0)
       store8_vec<float>(to, 8, r);
     else
-      store8_any<float>(to, n, r);
+      store_singly(to, n, r);
   };
   for (int i = 0; i < G; ++i) {
     if (grp == i) {
@@ -55,6 +65,25 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// A row of `bytes` at any address p, whose matrix is [lo, hi): the 16-byte words that hold it
+// and lie in the matrix, brought by a bulk copy to dst (a 16-byte boundary) on, and what of
+// the row they leave, elements of the matrix's first or last word, by this thread.
+struct AnyCopy {
+  uintptr_t from;
+  uint32_t skip, size;
+};
+template <typename T>
+__device__ __forceinline__ AnyCopy any_copy(uint8_t* dst, uintptr_t p, uint32_t bytes,
+                                            uintptr_t lo, uintptr_t hi) {
+  const uintptr_t s0 = p & ~static_cast<uintptr_t>(15), e1 = (p + bytes + 15) & ~static_cast<uintptr_t>(15);
+  const uintptr_t a0 = s0 >= lo ? s0 : s0 + 16, a1 = e1 <= hi ? e1 : e1 - 16;
+  for (uintptr_t e = p; e < a0; e += sizeof(T))
+    *reinterpret_cast<T*>(dst + (e - s0)) = *reinterpret_cast<const T*>(e);
+  for (uintptr_t e = a1; e < p + bytes; e += sizeof(T))
+    *reinterpret_cast<T*>(dst + (e - s0)) = *reinterpret_cast<const T*>(e);
+  return {a0, static_cast<uint32_t>(a0 - s0), static_cast<uint32_t>(a1 - a0)};
+}
+
 // W warps per row, G groups of them per CTA; with the ring, S stages of `stage` bytes for
 // each group.  goff: the offset of gamma's copy in dynamic shared memory; gvec: gamma
 // itself lies at a 16-byte boundary; sring: a stage holds the scales too.
@@ -71,12 +100,12 @@ enum NSource : int { N_FROM_X = 0, N_INT8 = 1, N_E4M3 = 2 };
 // at a time, and a thread keeps its columns from row to row, so that their sums stay in
 // registers and leave once, joined over the groups, as row blockIdx.x of `part`.
 // A row is read twice, before and after its sums.  KEEP holds it in registers in between,
-// in 16 bits and codes as it came, where J <= 2 leaves the registers for it: 36.3 against
-// 37.8 us at 8192 x 2048 bf16 with int8 codes and dres; with J = 4 they spill, 239 against
-// 161 us at 16384 x 8192.
+// in 16 bits and codes as it came, where J <= 2 leaves the registers for it: 27.6 against
+// 29.8 us at 8192 x 2048 bf16 with int8 codes; with J = 4 they spill, 148 against 131 us at
+// 16384 x 8192.
 // GS: gamma lies in shared memory, in fp32.  Else it is read from where it is: by short or
-// few rows, and by wide ones whose ring needs the room (4096 x 16384 bf16 with dres: 144
-// us; with gamma's copy and no ring 231).
+// few rows, and by wide ones whose ring needs the room (4096 x 16384 bf16 with dres: 115
+// us; with gamma's copy and no ring 247).
 // RING: a row's inputs come by bulk copies into a ring of shared-memory stages that the
 // group's first thread fills ahead, so that reads are in flight while a row's sums and
 // their barrier are waited for.  A stage is refilled once every thread has read it for the
@@ -110,22 +139,46 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
   const int ng = (a.cols + Q8_GROUP - 1) / Q8_GROUP, pitch = ng * Q8_GROUP;
   // Scales in the ring.  (ACC_FULL rows have whole 16-byte words of them.)
   const bool sr = RING && CK && J > 1 && (MODE == ACC_FULL || p.sring);
+  constexpr bool ANY = MODE == ACC_ANY;
   const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
-  const uint32_t nbytes = CK ? static_cast<uint32_t>(pitch) : bytes;
+  const uint32_t rbytes = static_cast<uint32_t>(ring_row(bytes, ANY));  // in a stage
+  const uint32_t nbytes = CK ? static_cast<uint32_t>(pitch) : rbytes;
   // A stage: dy, x or the codes, dres, the scales.
   auto fill = [&](uint32_t row, int s) {
     if (row >= static_cast<uint32_t>(rows) || *abort_flag) return;
     const long long r = row;
     const uint32_t bar = bars + 8u * s;
     const uint32_t dst = data + (grp * p.S + s) * p.stage;
-    mbar_arrive_expect_tx(bar, bytes + nbytes + (a.dres ? bytes : 0u) + (sr ? ng : 0));
-    bulk_load(dst, static_cast<const T*>(a.dy) + r * a.lddy, bytes, bar);
-    if (CK)
-      bulk_load(dst + bytes, a.q + r * pitch, nbytes, bar);
-    else
-      bulk_load(dst + bytes, static_cast<const T*>(a.x) + r * a.ldx, nbytes, bar);
-    if (a.dres)
-      bulk_load(dst + bytes + nbytes, static_cast<const T*>(a.dres) + r * a.lddres, bytes, bar);
+    if constexpr (ANY) {
+      uint8_t* to = dyn + RING_BARS + (grp * p.S + s) * p.stage;
+      auto plan = [&](const void* m, long long ld, uint32_t at) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(m);
+        return any_copy<T>(to + at, lo + r * ld * sizeof(T), bytes, lo,
+                           lo + ((rows - 1) * ld + a.cols) * sizeof(T));
+      };
+      AnyCopy cy = plan(a.dy, a.lddy, 0), cx = {}, cr = {};
+      if (!CK) cx = plan(a.x, a.ldx, rbytes);
+      if (a.dres) cr = plan(a.dres, a.lddres, rbytes + nbytes);
+      mbar_arrive_expect_tx(bar, cy.size + (CK ? nbytes : cx.size) + cr.size + (sr ? ng : 0));
+      bulk_load(dst + cy.skip, reinterpret_cast<const void*>(cy.from), cy.size, bar);
+      if (CK)
+        bulk_load(dst + rbytes, a.q + r * pitch, nbytes, bar);
+      else
+        bulk_load(dst + rbytes + cx.skip, reinterpret_cast<const void*>(cx.from), cx.size, bar);
+      if (a.dres)
+        bulk_load(dst + rbytes + nbytes + cr.skip, reinterpret_cast<const void*>(cr.from),
+                  cr.size, bar);
+    } else {
+      mbar_arrive_expect_tx(bar, bytes + nbytes + (a.dres ? bytes : 0u) + (sr ? ng : 0));
+      bulk_load(dst, static_cast<const T*>(a.dy) + r * a.lddy, bytes, bar);
+      if (CK)
+        bulk_load(dst + bytes, a.q + r * pitch, nbytes, bar);
+      else
+        bulk_load(dst + bytes, static_cast<const T*>(a.x) + r * a.ldx, nbytes, bar);
+      if (a.dres)
+        bulk_load(dst + bytes + nbytes, static_cast<const T*>(a.dres) + r * a.lddres, bytes,
+                  bar);
+    }
     if (sr) bulk_load(dst + p.stage - ng, a.scale + r * ng, ng, bar);
   };
   if (RING) __syncthreads();  // the barriers exist
@@ -140,7 +193,7 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
 #pragma unroll
     for (int k = 0; k < 4; ++k) dg[j][k] = db[j][k] = f2(0.0f);
   // Statistics come straight from global memory, one row ahead, and so do scales that are
-  // not in the ring (a few bytes per load, whose waits others share: 161 against 131
+  // not in the ring (a few bytes per load, whose waits others share: 149 against 131
   // us at 16384 x 8192 with e4m3 codes).
   constexpr int NSC = CK ? J : 1;
   uint32_t sc[NSC] = {};
@@ -176,11 +229,36 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     const long long r = row;
     const uint8_t* st = dyn + RING_BARS + (grp * p.S + s) * p.stage;
     if (RING) mbar_wait(bars + 8u * s, ph, abort_flag);
-    const T* dyp = RING ? reinterpret_cast<const T*>(st)
-                        : static_cast<const T*>(a.dy) + r * a.lddy;
-    const T* xp = RING ? reinterpret_cast<const T*>(st + bytes)
-                       : static_cast<const T*>(a.x) + (CK ? 0 : r * a.ldx);
-    const uint8_t* qp = RING ? st + bytes : a.q + (CK ? r * pitch : 0);
+    const T* dyg = static_cast<const T*>(a.dy) + r * a.lddy;
+    const T* xg = static_cast<const T*>(a.x) + (CK ? 0 : r * a.ldx);
+    const T* rg = static_cast<const T*>(a.dres) + r * a.lddres;
+    const uint8_t* qp = RING ? st + rbytes : a.q + (CK ? r * pitch : 0);
+    // Vector j of the row that lies at g, and `at` bytes into the stage.
+    auto row8 = [&](const T* g, uint32_t at, int j, uint32_t (&w)[WORDS<T>]) {
+      const int c = c0 + j * cstep;
+      if constexpr (ANY) {
+        read8_shared<T>(st + at + c * sizeof(T), reinterpret_cast<uintptr_t>(g) & 15u,
+                        a.cols - c < 8 ? a.cols - c : 8, w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < WORDS<T>; k += 4) {
+          const uint4 q = reinterpret_cast<const uint4*>(st + at + c * sizeof(T))[k / 4];
+          w[k] = q.x;
+          w[k + 1] = q.y;
+          w[k + 2] = q.z;
+          w[k + 3] = q.w;
+        }
+      }
+    };
+    auto get8 = [&](const T* g, uint32_t at, int j, F2 (&v)[4]) {
+      if constexpr (RING) {
+        uint32_t w[WORDS<T>];
+        row8(g, at, j, w);
+        words8<T>(w, v);
+      } else {
+        load8<T, MODE>(g, c0 + j * cstep, a.cols, v);
+      }
+    };
     if (sr)
 #pragma unroll
       for (int j = 0; j < NSC; ++j)
@@ -188,32 +266,30 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
           sc[j] = st[p.stage - ng + t / 4 + j * (cstep / 32)];
     const F2 rs = f2(rstd), less = f2(-mean);
     // Vector j: dy and n.  KEEP: as it was read, for the second time.
-    uint4 kd[KEEP ? J : 1];
+    uint32_t kd[KEEP ? J : 1][WORDS<T>], kx[KEEP && !CK ? J : 1][WORDS<T>];
     uint2 kq[KEEP && CK ? J : 1];
-    uint4 kx[KEEP && !CK ? J : 1];
     auto vector8 = [&](int j, bool again, F2 (&d)[4], F2 (&m)[4]) {
-      const int c = c0 + j * cstep;
       if constexpr (KEEP) {
-        if (!again) kd[j] = *reinterpret_cast<const uint4*>(dyp + c);
-        expand8<T>(kd[j], d);
+        if (!again) row8(dyg, 0, j, kd[j]);
+        words8<T>(kd[j], d);
       } else {
-        load8<T, MODE>(dyp, c, a.cols, d);
+        get8(dyg, 0, j, d);
       }
       if constexpr (CK) {
+        const int c = c0 + j * cstep;
         uint2 q = make_uint2(0u, 0u);
-        if constexpr (KEEP) {
-          if (!again) kq[j] = *reinterpret_cast<const uint2*>(qp + c);
-          q = kq[j];
-        } else if (MODE != ACC_ANY || c < pitch) {
-          q = *reinterpret_cast<const uint2*>(qp + c);
+        if (!KEEP || !again) {
+          if (!ANY || c < pitch) q = *reinterpret_cast<const uint2*>(qp + c);
+          if constexpr (KEEP) kq[j] = q;
         }
+        if constexpr (KEEP) q = kq[j];
         q8_decode8<SRC == N_INT8 ? DASH_Q8_INT8 : DASH_Q8_E4M3>(q, sc[j], m);
       } else {
         if constexpr (KEEP) {
-          if (!again) kx[j] = *reinterpret_cast<const uint4*>(xp + c);
-          expand8<T>(kx[j], m);
+          if (!again) row8(xg, rbytes, j, kx[j]);
+          words8<T>(kx[j], m);
         } else {
-          load8<T, MODE>(xp, c, a.cols, m);
+          get8(xg, rbytes, j, m);
         }
         // The difference first: x may lie far from zero.
 #pragma unroll
@@ -264,8 +340,6 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
     }
     const F2 m1 = f2(a.center ? -sum[0] * inv : 0.0f), m2 = f2(-sum[1] * inv);
     T* dxp = static_cast<T*>(a.dx) + r * a.lddx;
-    const T* rp = RING ? reinterpret_cast<const T*>(st + bytes + nbytes)
-                       : static_cast<const T*>(a.dres) + r * a.lddres;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (MODE == ACC_VEC && left(j) <= 0) continue;
@@ -275,7 +349,7 @@ __global__ void __launch_bounds__(32 * BWD_WARPS, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) gj[k] = f2_fma(nj[k], m2, gj[k] + m1) * rs;
       if (a.dres) {
-        load8<T, MODE>(rp, c0 + j * cstep, a.cols, rj);
+        get8(rg, rbytes + nbytes, j, rj);
 #pragma unroll
         for (int k = 0; k < 4; ++k) gj[k] = gj[k] + rj[k];
       }
@@ -318,7 +392,9 @@ dash_status backward_k(const NormBwdArgs& a, const BwdPlan& b, RowPlan p, float*
 template <typename T, int SRC, int J>
 dash_status backward_j(const NormBwdArgs& a, const BwdPlan& b, float* part, cudaStream_t st) {
   RowPlan p = {b.W, b.G, b.S, b.stage, 0, false, b.sring};
-  if (!b.vec) return backward_k<T, SRC, J, ACC_ANY, false, true>(a, b, p, part, st);
+  if (!b.vec)
+    return b.S == 0 ? backward_k<T, SRC, J, ACC_ANY, false, true>(a, b, p, part, st)
+                    : backward_k<T, SRC, J, ACC_ANY, true, true>(a, b, p, part, st);
   if (b.S == 0) return backward_k<T, SRC, J, ACC_VEC, false, false>(a, b, p, part, st);
   const bool full = b.full;
   if constexpr (J > 1) {

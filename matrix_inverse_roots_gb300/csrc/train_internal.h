@@ -96,6 +96,11 @@ constexpr int BWD_WARPS = 16;                        // of a backward CTA, at mo
 constexpr int RING_MAX = 8;                          // most stages of a group
 constexpr int RING_BARS = 8 * BWD_WARPS * RING_MAX;  // their barriers
 constexpr size_t BWD_SMEM = 208 * 1024;              // dynamic; 16 KB more are static
+// Bytes of a ring stage for a row of `bytes`.  At any address a row starts up to 15 bytes
+// into its first 16-byte word, and is read up to 16 bytes past its last.
+constexpr size_t ring_row(size_t bytes, bool any) {
+  return any ? (bytes + 30) / 16 * 16 + 16 : bytes;
+}
 inline size_t gamma_room(int cols) { return (static_cast<size_t>(cols) + 7) / 8 * 32; }
 dash_status norm_backward_f32(const NormBwdArgs& a, const BwdPlan& b, float* part,
                               cudaStream_t st);
