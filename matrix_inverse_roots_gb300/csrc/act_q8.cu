@@ -4,8 +4,6 @@
 // (four neighbouring lanes share a group, so its largest magnitude takes two shuffles) and
 // issues all their loads before the first use: Q8_U of them, 16 to 32 KB of reads in
 // flight per 256 threads.
-#include <type_traits>
-
 #include "act_q8.cuh"
 #include "dash_internal.h"
 #include "train_internal.h"
@@ -26,31 +24,18 @@ __global__ void __launch_bounds__(Q8_THREADS)
   const unsigned v0 = FLAT ? 0 : static_cast<unsigned>(base - row0 * nv);
   const T* x = static_cast<const T*>(a.x);
   F2 v[Q8_U][4];
-  // Whether all rows of the tile are inner ones.
-  const bool inner = MODE == ACC_ANY && inner_row<T>(row0, a.rows, a.cols) &&
-                     row0 + (v0 + Q8_THREADS * Q8_U - 1) / nv < a.rows - 1;
-  auto load = [&](auto in) {
 #pragma unroll
-    for (int u = 0; u < Q8_U; ++u) {
-      const unsigned off = u * Q8_THREADS + threadIdx.x;
-      const long long i = base + off;
-      if (FLAT) {
-        load8_vec<T>(x + i * 8, i < total ? 8 : 0, v[u]);
-      } else {
-        const unsigned k = (v0 + off) / nv;
-        const int c = static_cast<int>(v0 + off - k * nv) * 8;
-        const T* row = x + (row0 + k) * a.ld;
-        if constexpr (decltype(in)::value)
-          load8_inner<T>(row + c, static_cast<int>(a.cols) - c, v[u]);
-        else
-          load8<T, MODE>(row, c, i < total ? static_cast<int>(a.cols) : c, v[u]);
-      }
+  for (int u = 0; u < Q8_U; ++u) {
+    const unsigned off = u * Q8_THREADS + threadIdx.x;
+    const long long i = base + off;
+    if (FLAT) {
+      load8_vec<T>(x + i * 8, i < total ? 8 : 0, v[u]);
+    } else {
+      const unsigned k = (v0 + off) / nv;
+      const int c = static_cast<int>(v0 + off - k * nv) * 8;
+      load8<T, MODE>(x + (row0 + k) * a.ld, c, i < total ? static_cast<int>(a.cols) : c, v[u]);
     }
-  };
-  if (inner)
-    load(std::true_type());
-  else
-    load(std::false_type());
+  }
 #pragma unroll
   for (int u = 0; u < Q8_U; ++u) {
     const long long i = base + u * Q8_THREADS + threadIdx.x;

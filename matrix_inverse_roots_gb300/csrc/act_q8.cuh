@@ -176,7 +176,9 @@ __device__ __forceinline__ uint32_t pack2(F2 a) {
 enum Access : int { ACC_ANY = 0, ACC_VEC = 1, ACC_FULL = 2 };  // FULL: all exist
 
 // Eight elements from p at any address, of which n exist; the others are zero.  (Read
-// singly; the first and last rows of a matrix, and short ones.)
+// singly: L1 serves a warp's 512 bytes to its eight loads.  Aligned 16-byte words shifted
+// into place took as long, 63 against 55 us for the norm's forward pass at 13696 x 1603 bf16
+// with a residual, 20 each for act_compress.)
 template <typename T>
 __device__ __forceinline__ void load8_any(const T* p, int n, F2 (&v)[4]) {
 #pragma unroll
@@ -279,37 +281,9 @@ __device__ __forceinline__ void words8(const uint32_t (&w)[WORDS<T>], F2 (&v)[4]
   }
 }
 
-// Whether 16-byte words that hold elements of this row lie in its matrix: not of the first
-// and last row, whose words may begin before the matrix or end past it.
-template <typename T>
-__device__ __forceinline__ bool inner_row(long long row, long long rows, long long cols) {
-  return row > 0 && row < rows - 1 && cols * static_cast<int>(sizeof(T)) >= 16;
-}
-
-// Eight elements at any address p in an inner row, of which n exist (any n); the others are
-// zero.  Aligned 16-byte words, two (three of fp32), shifted into place.
-template <typename T>
-__device__ __forceinline__ void load8_inner(const T* p, int n, F2 (&v)[4]) {
-  n = n < 8 ? n : 8;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const int off = static_cast<int>(at & 15u);
-  const uint4* f = reinterpret_cast<const uint4*>(at - off);
-  uint32_t w[WORDS<T> + 4], out[WORDS<T>];
-#pragma unroll
-  for (int k = 0; k < WORDS<T> + 4; k += 4) {
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    if (n > 0 && 4 * k - off < n * static_cast<int>(sizeof(T))) q = f[k / 4];
-    w[k] = q.x;
-    w[k + 1] = q.y;
-    w[k + 2] = q.z;
-    w[k + 3] = q.w;
-  }
-  cut8<T>(w, off, n, out);
-  words8<T>(out, v);
-}
-
-// The same from shared memory: p is the 16-byte boundary before the elements, off their
-// distance from it.  Reads 16 bytes more than the elements take.
+// Eight elements in shared memory, of which n exist (any n); the others are zero.  p is the
+// 16-byte boundary before them, off their distance from it.  Reads 16 bytes more than the
+// elements take.
 template <typename T>
 __device__ __forceinline__ void read8_shared(const uint8_t* p, uint32_t off, int n,
                                              uint32_t (&out)[WORDS<T>]) {
@@ -329,19 +303,17 @@ __device__ __forceinline__ void read8_shared(const uint8_t* p, uint32_t off, int
 // Eight elements to columns c .. c + 7 of a row at any address; lane l of the warp has
 // columns c0 + 8 l, and the whole warp calls.  A lane stores the aligned 16-byte words that
 // begin in its elements, with the next lane's first bytes; what a warp or a row begins or
-// ends with goes singly.  (All of it singly: 63 against 31 us for act_restore of
-// 13696 x 1603 bf16.)
+// ends with goes in aligned pieces of 8, 4 and 2 bytes.  (Elements singly: 63 us for
+// act_restore of 13696 x 1603 bf16; only the ends singly: 29 us; as here: 22 us.)
 template <typename T>
 __device__ __forceinline__ void store8_joined(T* row, int c, int cols, const F2 (&v)[4]) {
-  constexpr int N = static_cast<int>(sizeof(T)) * 2;
-  constexpr int B = 8 * static_cast<int>(sizeof(T));
-  const uintptr_t r1 = reinterpret_cast<uintptr_t>(row) + cols * sizeof(T);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + static_cast<uintptr_t>(c) * sizeof(T);
-  const uint32_t off = static_cast<uint32_t>(at & 15u);
+  constexpr int N = WORDS<T>, SZ = static_cast<int>(sizeof(T)), B = 8 * SZ;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+  const int off = static_cast<int>(at & 15u);
   uint32_t w[N + 4], out[N];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (SZ == 4) {
       float lo, hi;
       f2_get(v[k], lo, hi);
       w[2 * k] = __float_as_uint(lo);
@@ -351,38 +323,82 @@ __device__ __forceinline__ void store8_joined(T* row, int c, int cols, const F2 
     }
   }
   const int lane = threadIdx.x & 31;
-  const uint32_t head = off ? 16u - off : 0u;  // own bytes before the first boundary
+  const int left = (cols - c) * SZ;      // bytes of the row from here on
+  const int head = (16 - off) & 15;      // own bytes before the first boundary
   const uintptr_t f = at + head;
-  // Whether this lane stores whole words [f, f + B), and whether the lane before does (its
-  // words end at f and hold this lane's head).
-  const bool whole = f + B <= r1 && (off == 0 || lane < 31);
-  const bool covered = off == 0 || (lane > 0 && f <= r1);
-  uint32_t own[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) own[k] = w[k];
   if (off != 0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[N + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
-    shift_words<N>(w, head, out);
+    uint32_t x[N + 4];
+#pragma unroll
+    for (int k = 0; k < N + 4; ++k) x[k] = w[k];
+    shift_words<N>(x, head, out);
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) out[k] = w[k];
   }
-  if (whole)
+  if (head + B <= left && (off == 0 || lane < 31)) {
 #pragma unroll
     for (int k = 0; k < N; k += 4)
       *reinterpret_cast<uint4*>(f + 4 * k) = make_uint4(out[k], out[k + 1], out[k + 2], out[k + 3]);
-  if (!whole || !covered) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uintptr_t e = at + k * sizeof(T);
-      if (e < r1 && (e < f ? !covered : !whole)) {
-        if constexpr (sizeof(T) == 4)
-          *reinterpret_cast<uint32_t*>(e) = own[k];
-        else
-          *reinterpret_cast<uint16_t*>(e) =
-              static_cast<uint16_t>(own[k / 2] >> (16 * (k & 1)));
+  } else if (left > head) {
+    // Own bytes after the boundary, fewer than eight elements'.
+    const int m = (left < B ? left : B) - head;
+    uintptr_t p = f;
+    uint32_t a = out[0], b = out[1], e = out[2];
+    if constexpr (SZ == 4) {
+      if (m & 16) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(out[0], out[1], out[2], out[3]);
+        a = out[4];
+        b = out[5];
+        e = out[6];
+        p += 16;
       }
+    }
+    if (m & 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+      a = e;
+      b = out[3];
+      p += 8;
+    }
+    if (m & 4) {
+      *reinterpret_cast<uint32_t*>(p) = a;
+      a = b;
+      p += 4;
+    }
+    if (SZ == 2 && (m & 2)) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(a);
+  }
+  // The bytes before the boundary, unless the lane before has stored them with its last word.
+  if (off != 0 && left > 0 && !(lane > 0 && head <= left)) {
+    if (head <= left) {
+      uintptr_t p = at;
+      uint32_t a = w[0], b = w[1], e = w[2];
+      if constexpr (SZ == 2) {
+        if (head & 2) {
+          *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(a);
+          a = __funnelshift_r(w[0], w[1], 16);
+          b = __funnelshift_r(w[1], w[2], 16);
+          e = __funnelshift_r(w[2], w[3], 16);
+          p += 2;
+        }
+      }
+      if (head & 4) {
+        *reinterpret_cast<uint32_t*>(p) = a;
+        a = b;
+        b = e;
+        p += 4;
+      }
+      if (head & 8) *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k * SZ < left) {
+          if constexpr (SZ == 4)
+            *reinterpret_cast<uint32_t*>(at + 4 * k) = w[k];
+          else
+            *reinterpret_cast<uint16_t*>(at + 2 * k) =
+                static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+        }
     }
   }
 }
@@ -419,17 +435,18 @@ __device__ __forceinline__ void load8_dt(const void* p, int dt, bool vec, int64_
                                          F2 (&v)[4]) {
   if (vec && n >= 8) {
     if (dt == DASH_DT_F32)
-      load8_vec<float>(static_cast<const float*>(p) + i, 8, v);
+      load8_vec(static_cast<const float*>(p) + i, 8, v);
     else if (dt == DASH_DT_BF16)
-      load8_vec<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(p) + i, 8, v);
+      load8_vec(static_cast<const __nv_bfloat16*>(p) + i, 8, v);
     else
-      load8_vec<__half>(static_cast<const __half*>(p) + i, 8, v);
-    return;
+      load8_vec(static_cast<const __half*>(p) + i, 8, v);
+  } else if (dt == DASH_DT_F32) {
+    load8_any(static_cast<const float*>(p) + i, n, v);
+  } else if (dt == DASH_DT_BF16) {
+    load8_any(static_cast<const __nv_bfloat16*>(p) + i, n, v);
+  } else {
+    load8_any(static_cast<const __half*>(p) + i, n, v);
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    v[k] = f2(2 * k < n ? load_dt(p, dt, i + 2 * k) : 0.0f,
-              2 * k + 1 < n ? load_dt(p, dt, i + 2 * k + 1) : 0.0f);
 }
 
 // Largest magnitude (bits; NaN's are above infinity's) of the group that this lane shares
