@@ -220,11 +220,11 @@ dash_status launch_part_sum(const float* part, int parts, long long cols, float*
   return part_sum(part, parts, cols, cols, out, nullptr, st);
 }
 
-// Slices of the rows: four CTAs per SM, each warp of one with 16 rows or more.
+// Slices of the rows: four CTAs per SM, each warp of one with four rows or more.
 int col_sum_parts(long long rows, long long cols) {
   const long long tiles = (cols + 255) / 256;
   const long long want = tiles > 0 ? (152 * 4 + tiles - 1) / tiles : 1;
-  const long long most = (rows + 16 * CS_WARPS - 1) / (16 * CS_WARPS);
+  const long long most = (rows + 4 * CS_WARPS - 1) / (4 * CS_WARPS);
   const long long p = want < most ? want : most;
   return static_cast<int>(p < 1 ? 1 : p);
 }

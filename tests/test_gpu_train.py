@@ -595,6 +595,27 @@ def test_weight_grad_at_the_ends_of_the_scale(exp, fmt):
     assert dr.device_status() == 0
 
 
+@pytest.mark.parametrize("odt", DTYPES)
+@pytest.mark.parametrize("off", range(8))
+@pytest.mark.parametrize("cols,ld", [(1, 3), (15, 15), (17, 23), (255, 257), (530, 531)])
+def test_weight_grad_stores_any_alignment(cols, ld, off, odt):
+    """dW rows that begin and end anywhere: the same bits as aligned ones, and nothing
+    outside them."""
+    require_gpu()
+    dr = library()
+    rows, outs = 70, 300
+    dtype = torch.float32 if off % 2 else torch.bfloat16
+    q, s = dr.act_compress(randn((rows, cols), 64))
+    dz = randn((rows, outs), 65, dtype)
+    gamma, beta = randn((cols,), 66), randn((cols,), 67)
+    wide = strided(torch.zeros((outs, cols), dtype=odt, device="cuda"), -(-cols // 8) * 8)
+    dr.weight_grad(dz, q, s, cols, gamma=gamma, beta=beta, out=wide)
+    out = strided(torch.zeros((outs, cols), dtype=odt, device="cuda"), ld, off)
+    dr.weight_grad(dz, q, s, cols, gamma=gamma, beta=beta, out=out)
+    assert (out == wide).all() and gaps_untouched(out) and gaps_untouched(wide)
+    assert dr.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_weight_grad_of_strided_views(dtype):
     require_gpu()
