@@ -12,6 +12,7 @@ computation runs in the library's CUDA kernels.  There is no fallback: if
 
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -635,6 +636,11 @@ def _begin():
     return _lib or load_library(), dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _device():
+    """The current device, which sizes depend on; -1 without one."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
 def _refuse(t, name, dev, what):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
@@ -792,12 +798,17 @@ def layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, center=True, residual
     return NormForward(y, mean, rstd, r, q, scale)
 
 
-def layer_norm_workspace_size(rows, cols):
-    """Workspace bytes of layer_norm_backward."""
+@functools.lru_cache(maxsize=256)
+def _layer_norm_ws(rows, cols, dev):
     out = ctypes.c_size_t(0)
     _check(load_library().dash_layer_norm_workspace_size(rows, cols, ctypes.byref(out)),
            "dash_layer_norm_workspace_size")
     return out.value
+
+
+def layer_norm_workspace_size(rows, cols):
+    """Workspace bytes of layer_norm_backward."""
+    return _layer_norm_ws(rows, cols, _device())
 
 
 def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=None, fmt="int8",
@@ -840,7 +851,7 @@ def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=N
     else:
         lddx = _rows(dx, "dx", dev, dtype, shape)
     if ws is None and (gamma is not None or beta):
-        ws = torch.empty(max(layer_norm_workspace_size(rows, cols), 256), dtype=torch.uint8,
+        ws = torch.empty(max(_layer_norm_ws(rows, cols, dev), 256), dtype=torch.uint8,
                          device=dy.device)
     e = lib.layer_norm_backward(dy.data_ptr(), lddy, _DTYPES.get(dtype, -1), rows, cols, _addr(x),
                                 ldx, pm, _addr(q), _addr(scale), f, ps, g, wdt,
@@ -851,16 +862,22 @@ def layer_norm_backward(dy, rstd, gamma=None, x=None, mean=None, q=None, scale=N
     return dx, dgamma, dbeta
 
 
+@functools.lru_cache(maxsize=256)
+def _weight_grad_ws(rows, outs, cols, dt, odt, lddz, B, dev):
+    out = ctypes.c_size_t(0)
+    _check(load_library().dash_weight_grad_workspace_size(rows, outs, cols, dt, odt, lddz, B,
+                                                          ctypes.byref(out)),
+           "dash_weight_grad_workspace_size")
+    return out.value
+
+
 def weight_grad_workspace_size(rows, outs, cols, dtype=torch.bfloat16, B=None, lddz=0,
                                out_dtype=None):
     """Workspace bytes of weight_grad for dz of `dtype` and dW of `out_dtype` (the same by
     default).  lddz: the row stride of a dz whose address is a multiple of 16 bytes; 0
     covers any dz."""
-    out = ctypes.c_size_t(0)
-    _check(load_library().dash_weight_grad_workspace_size(
-        rows, outs, cols, _DTYPES.get(dtype, -1), _DTYPES.get(out_dtype or dtype, -1), lddz,
-        int(B or 0), ctypes.byref(out)), "dash_weight_grad_workspace_size")
-    return out.value
+    return _weight_grad_ws(rows, outs, cols, _DTYPES.get(dtype, -1),
+                           _DTYPES.get(out_dtype or dtype, -1), lddz, int(B or 0), _device())
 
 
 def weight_grad(dz, q, scale, cols, fmt="int8", gamma=None, beta=None, B=None, dtype=None,
@@ -887,8 +904,8 @@ def weight_grad(dz, q, scale, cols, fmt="int8", gamma=None, beta=None, B=None, d
     db = torch.empty(outs, dtype=torch.float32, device=dz.device) if bias else None
     pz = dz.data_ptr()
     if ws is None:
-        n = weight_grad_workspace_size(rows, outs, cols, dz.dtype, B, 0 if pz & 15 else lddz,
-                                       out.dtype)
+        n = _weight_grad_ws(rows, outs, cols, _DTYPES.get(dz.dtype, -1),
+                            _DTYPES.get(out.dtype, -1), 0 if pz & 15 else lddz, B, dev)
         ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dz.device)
     e = lib.weight_grad(pz, _DTYPES.get(dz.dtype, -1), lddz, rows, outs, q.data_ptr(),
                         scale.data_ptr(), f, cols, g, b, wdt, out.data_ptr(), _gdt(out), ldw, B,
