@@ -104,6 +104,7 @@ struct WParams {
   int units;
   int bn;
   int vec_out;         // rows of dW take 16-byte stores
+  int pad;             // the padding is the product kernel's
   long long rows, ng;
   const uint8_t* scale;
   const float* db;     // column sums of dz (null without beta)
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
       }
       ahead = kb - x.k1;
     }
-    if (warp == 9)
+    if (warp == 9 && p.pad)
       pad_zero(p.a, static_cast<long long>(p.tiles_m) * WM, static_cast<long long>(p.tiles_n) * BN,
                static_cast<long long>(blockIdx.x) * 32 + lane,
                static_cast<long long>(gridDim.x) * 32);
@@ -846,6 +847,30 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// The same for much padding: a warp per row of a block, all SMs.  (Left to one warp of each of
+// the product's CTAs, few where dW is small, a gradient of 448 x 192 in a 1024-block took
+// 446 us, with this launch 14.)
+__global__ void __launch_bounds__(256)
+    weight_grad_pad_kernel(const WeightGradArgs a, long long r0, long long c0) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long b = a.block, pr = padded(a.outs, a.block), nbc = padded(a.cols, a.block) / b;
+  const int lane = threadIdx.x & 31;
+  const long long n = static_cast<long long>(gridDim.x) * 8;
+  for (long long e = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); e < pr * nbc;
+       e += n) {
+    const long long o = e / nbc, k = e - o * nbc;
+    const long long from = o >= r0 ? 0 : c0 - k * b;  // first column of the block's row
+    const long long at = dw_row(a, o) + k * b * b;
+    for (long long c = (from > 0 ? from : 0) + lane * 4; c < b; c += 128) {
+      if (a.odt == DASH_DT_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at + c) =
+            make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dw) + at + c) = make_uint2(0u, 0u);
+    }
   }
 }
 
@@ -1245,10 +1270,31 @@ dash_status launch_weight_grad(const WeightGradArgs& a, void* ws, cudaStream_t s
     }
     const WInst k = inst_of(a.fmt, plan.bn, plan.parts);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (plan.units < pairs ? plan.units : pairs)), 1, 1);
+    // Padding beyond the tiles: by an idle warp of each CTA where it is done before the
+    // product is (4 ns per element; a slot 0.4 us, see make_plan, and 8 us around them), or
+    // by a launch of its own: 8192 x 5632 x 2048 in 1024-blocks 132 against 138 us, but
+    // 300 x 1100 x 2000 83 against 20.
+    const long long r0 = static_cast<long long>(plan.tiles_m) * WM;
+    const long long c0 = static_cast<long long>(plan.tiles_n) * plan.bn;
+    const long long pr = padded(a.outs, a.block), pc = padded(a.cols, a.block);
+    const long long pad = pr * pc - (r0 < pr ? r0 : pr) * (c0 < pc ? c0 : pc);
+    const double slots = static_cast<double>(plan.units) / pairs * plan.kper;
+    const double product_us = 8.0 + 0.4 * slots * plan.parts * plan.bn / 256.0;
+    p.pad = 0.004 * pad <= product_us * cfg.gridDim.x;
+    if (!p.pad) {
+      const dim3 grid = cfg.gridDim;
+      const long long need = (pr * (pc / a.block) + 7) / 8;
+      const long long cap = static_cast<long long>(device_sm_count()) * 8;
+      cfg.gridDim = dim3(static_cast<unsigned>(need < cap ? need : cap));
+      cfg.blockDim = dim3(256);
+      cfg.numAttrs = attrs(at, false);
+      err = cudaLaunchKernelEx(&cfg, weight_grad_pad_kernel, a, r0, c0);
+      cfg.gridDim = grid;
+    }
     cfg.blockDim = dim3(W_THREADS, 1, 1);
     cfg.dynamicSmemBytes = k.smem;
     cfg.numAttrs = attrs(at, true);
-    err = cudaLaunchKernelEx(&cfg, k.k, tA, tQ, p);
+    if (err == cudaSuccess) err = cudaLaunchKernelEx(&cfg, k.k, tA, tQ, p);
   }
   const int tiles = plan.tiles_m * plan.tiles_n;
   if (a.rows == 0) {

@@ -786,3 +786,22 @@ def test_python_refusals():
             call()
     torch.cuda.synchronize()
     assert dr.device_status() == 0
+
+
+@pytest.mark.parametrize("rows,outs,cols,B", [(2, 448, 192, 1024), (3, 153, 1200, 1024),
+                                              (40, 300, 70, 512), (5, 129, 129, 384)])
+@pytest.mark.parametrize("odt", [torch.float32, torch.bfloat16])
+def test_weight_grad_blocks_of_mostly_padding(rows, outs, cols, B, odt):
+    """Few small tiles in large blocks: the same values as the matrix, zeros everywhere
+    else, from a buffer of NaN."""
+    require_gpu()
+    dr = library()
+    q, s = dr.act_compress(randn((rows, cols), 70))
+    dz = randn((rows, outs), 71, torch.bfloat16)
+    dw, _ = dr.weight_grad(dz, q, s, cols, dtype=odt)
+    nb = -(-outs // B) * -(-cols // B)
+    out = torch.full((nb, B, B), float("nan"), dtype=odt, device="cuda")
+    dr.weight_grad(dz, q, s, cols, B=B, out=out)
+    want, _, _ = dr.pack_blocks(dw, B)
+    assert (out == want).all()
+    assert dr.device_status() == 0
